@@ -341,6 +341,147 @@ int wq_describe_plan_gs(int fmt, int O, int I, int S, int gs, char *buf, size_t 
 int wq_stream_read_dev(const void *buf_dev, size_t bytes, int waves, int loads_in_flight, unsigned *out_dev,
                        void *hip_stream);
 
+/* ------------------------------------------------------------------------
+ * Between a decoder layer's products: the norm before a product, rotary
+ * positions of queries and keys, the quantised key/value cache and the
+ * attention of new tokens over it. All calls are stream-ordered on hip_stream
+ * (a hipStream_t; NULL = the null stream) with device buffers, queue their
+ * work without host synchronisation, may be captured into a HIP graph, need
+ * wq_init on the device, and give the same bits for the same inputs and the
+ * same launch configuration. Strides are in elements unless said otherwise;
+ * the last dimension of every buffer is contiguous. Buffers must be aligned
+ * to their element type; 16-byte aligned rows take the wide loads and others
+ * a slower path with the same results. WQ_FAULT=launch makes each of them
+ * return WQ_E_FAULT.
+ */
+enum wq_dtype { WQ_DT_F32 = 0, WQ_DT_BF16 = 1, WQ_DT_F16 = 2, WQ_DT_I8 = 3 };
+
+#define WQ_NORM_MAX_N 32768 /* longest row of wq_rmsnorm_dev */
+#define WQ_ROPE_MAX_ROT 256 /* most rotated elements of a head */
+#define WQ_ROPE_MAX_AXES 8
+#define WQ_KV_MAX_HEADS 1024 /* most heads of a cache or of queries */
+
+/*
+ * Root-mean-square norm, with the residual's addition:
+ *     r = x + residual            (in fp32; residual NULL: r = x)
+ *     y = r / sqrt(mean(r^2) + eps) * w
+ * x, residual, sum_out: [rows, n] of x_dtype (f32, bf16, f16), row strides
+ * x_stride, res_stride, sum_stride; w: n floats; y: [rows, n] of y_dtype, row
+ * stride y_stride. sum_out (NULL: not kept) receives r rounded to x_dtype;
+ * the norm is taken of the unrounded r. y_dtype WQ_DT_I8 needs y_scale (rows
+ * floats): y_scale = max|y| / 127 and the codes are
+ * rint(127 * (r*w) / max|r*w|), the quotient in fp64, so y ~ code * y_scale;
+ * a row of zeros gets codes 0 and scale 0, a row holding an infinity or a
+ * NaN codes 0 and a NaN scale. sum_out may be x or residual (same stride), and
+ * y may be x when the types and strides agree.
+ * n <= WQ_NORM_MAX_N (WQ_E_UNSUPPORTED above); rows == 0 is a no-op.
+ */
+int wq_rmsnorm_dev(int device, const void *x, int x_dtype, long x_stride, const void *residual, long res_stride,
+                   const float *w, float eps, int rows, int n, void *y, int y_dtype, long y_stride, float *y_scale,
+                   void *sum_out, long sum_stride, void *hip_stream);
+
+/*
+ * Rotary positions. The first `rot` elements of a head (even, at most
+ * WQ_ROPE_MAX_ROT) form rot/2 pairs; pair i is (x[i], x[i + rot/2]) with
+ * pairing 0 and (x[2i], x[2i+1]) with pairing 1, and is turned by the angle
+ *     pos[axis(i)] * theta^(-2i / rot),
+ * where the pairs are dealt to the axes in order: the first sections[0] pairs
+ * follow axis 0, the next sections[1] axis 1, and so on (one axis: text;
+ * three: time, height and width). Elements past rot are copied. Angles are
+ * reduced in fp64, so far positions keep fp32 accuracy.
+ *
+ * wq_rope_create makes the plan (host memory only; sections: host array of
+ * `axes` non-negative counts with sum rot/2; theta > 0); wq_rope_free
+ * releases it (NULL is a no-op). wq_rope_dev turns x [T, H, D] (strides
+ * x_tok, x_head) into y (y_tok, y_head; may be x itself with x's strides);
+ * pos: device int32 [axes, T] with row stride pos_stride.
+ */
+typedef struct wq_rope wq_rope;
+int wq_rope_create(int rot, int pairing, double theta, const int *sections, int axes, wq_rope **rope);
+int wq_rope_dev(const wq_rope *rope, int device, const void *x, int dtype, int T, int H, int D, long x_tok,
+                long x_head, const int *pos_dev, long pos_stride, void *y, long y_tok, long y_head, void *hip_stream);
+int wq_rope_free(wq_rope *rope);
+
+/*
+ * A paged, quantised key/value cache: pools the caller owns. A row holds the
+ * D = dim codes of one token and head and stands for code * scale:
+ *   WQ_KV_F16  2 bytes a code, IEEE half; the scale is a power of two that
+ *              puts the row's largest magnitude into [2^14, 2^15];
+ *   WQ_KV_I8   1 byte, two's complement, scale = max|x| / 127;
+ *   WQ_KV_I4   2 codes a byte, even element in the low half, stored as
+ *              code + 8 with codes -7..7, scale = max|x| / 7.
+ * Row (page, head, slot) starts at page*row_stride[0] + head*row_stride[1] +
+ * slot*row_stride[2] BYTES from k (and from v), its scale at the same sum of
+ * scale_stride (in floats) from k_scale (v_scale); k, v and row_stride are
+ * multiples of 16 bytes. dim is 64, 128 or 256; `page` slots a page (any
+ * number >= 1), `pages` pages, `heads` key/value heads.
+ *
+ * A batch: the new tokens of B sequences stand one after another, sequence b's
+ * at q_start[b] .. q_start[b+1]-1 (device int32 [B+1], ascending from 0 to T);
+ * they are the last of its kv_len[b] positions (device int32 [B]), so the i-th
+ * new token has position p = kv_len[b] - q_len[b] + i. Position t lies in slot
+ * t % page of page table[b*table_stride + t / page] (device int32, `width`
+ * entries a sequence; entries past a sequence's end are not read as pages).
+ * max_q and max_kv: the longest q_len and kv_len (0: not known); they choose
+ * the split of the work only, results are right for any lengths.
+ * Positions outside the table, and those whose entry is outside [0, pages),
+ * are not there: append skips them, read gives zeros, attention does not see
+ * them. Nothing is read or written outside the pools and the T tokens,
+ * whatever q_start, kv_len and table hold.
+ */
+enum wq_kv_kind { WQ_KV_F16 = 0, WQ_KV_I8 = 1, WQ_KV_I4 = 2 };
+
+typedef struct wq_kv_cache {
+    int device, kind, pages, heads, page, dim;
+    void *k, *v;
+    float *k_scale, *v_scale;
+    long row_stride[3];
+    long scale_stride[3];
+} wq_kv_cache;
+
+typedef struct wq_kv_batch {
+    int B, T, width, max_q, max_kv;
+    long table_stride;
+    const int *q_start, *kv_len, *table;
+} wq_kv_batch;
+
+/*
+ * Quantise the T new tokens' keys and values ([T, heads, dim] of dtype f32,
+ * bf16 or f16, strides tok, head for both) into their slots. Codes are
+ * rint(x / scale), the quotient in fp64 (ties to even). A row whose largest
+ * magnitude is below 2^-100 is stored as zeros with scale 0; a row holding an
+ * infinity or a NaN as zero codes with a NaN scale.
+ */
+int wq_kv_append_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *k_new, const void *v_new,
+                     int dtype, long tok, long head, void *hip_stream);
+
+/* The values the batch's T tokens have in the cache, code * scale in fp32
+ * rounded to dtype, as k_out, v_out [T, heads, dim] with strides tok, head. */
+int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_out, void *v_out, int dtype, long tok,
+                   long head, void *hip_stream);
+
+/*
+ * Attention of the batch's new tokens over the cache. For token i of sequence
+ * b with position p, and query head h reading key/value head h / (H/heads):
+ *     s_t = scale * q . k_t,   w = softmax of s over the seen positions t,
+ *     o = sum_t w_t v_t,       lse = log sum_t exp(s_t),
+ * where t is seen if 0 <= t < kv_len[b], t <= p (causal) and t > p - window
+ * (window > 0). A token that sees nothing gets o = 0 and lse = -inf. What
+ * unseen positions hold (infinities and NaN among it) never enters a result.
+ * q, o: [T, H, dim] of dtype (f32, bf16, f16) with strides; H a multiple of
+ * the cache's heads; lse: float [T, H], contiguous, or NULL. The softmax
+ * statistics and all sums are fp32. f32 queries and probabilities enter the
+ * matrix units as two f16 parts (22 bits and more), bf16/f16 queries exactly,
+ * their probabilities rounded to f16 (2^-12, below the output's rounding); the
+ * codes are exact.
+ * Where the positions are split among blocks, partial results pass through
+ * the stream's workspace as in wq_matmul_dev (it may grow; while the stream
+ * is being captured it cannot: warm up first, else WQ_E_UNSUPPORTED).
+ */
+int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *q, int dtype, int H, long q_tok,
+                      long q_head, float scale, int causal, int window, void *o, long o_tok, long o_head, float *lse,
+                      void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,6 +35,12 @@ WQ_E_MISMATCH = -5
 WQ_E_HIP = -6
 WQ_E_FAULT = -7
 WQ_E_UNSUPPORTED = -8
+WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16, WQ_DT_I8 = 0, 1, 2, 3
+WQ_KV_F16, WQ_KV_I8, WQ_KV_I4 = 0, 1, 2
+WQ_NORM_MAX_N = 32768
+WQ_ROPE_MAX_ROT = 256
+WQ_ROPE_MAX_AXES = 8
+WQ_KV_MAX_HEADS = 1024
 WQ_MAX_DEVICES = 16
 WQ_GEMV_MAX_S = 8
 
@@ -45,6 +51,17 @@ _c_int_p = ctypes.POINTER(ctypes.c_int)
 _c_size_p = ctypes.POINTER(ctypes.c_size_t)
 
 
+class _KvCacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("device", "kind", "pages", "heads", "page", "dim")] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        ("row_stride", ctypes.c_long * 3), ("scale_stride", ctypes.c_long * 3)]
+
+
+class _KvBatchC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "width", "max_q", "max_kv")] + [
+        ("table_stride", ctypes.c_long)] + [(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "table")]
+
+
 class WqError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -53,6 +70,7 @@ class WqError(RuntimeError):
 
 def _bind(lib):
     vp, ci, cl = ctypes.c_void_p, ctypes.c_int, ctypes.c_long
+    cf, cachep, batchp = ctypes.c_float, ctypes.POINTER(_KvCacheC), ctypes.POINTER(_KvBatchC)
     sig = {
         "wq_init": (ci, [_c_int_p, ci]),
         "wq_mem_info": (ci, [ci, _c_size_p, _c_size_p]),
@@ -76,6 +94,13 @@ def _bind(lib):
         "wq_stream_read_dev": (ci, [vp, ctypes.c_size_t, ci, ci, vp, vp]),
         "wq_matmul_dev_noalloc": (ci, [vp, vp, ci, vp, vp]),
         "wq_noalloc_scratch_bytes": (ctypes.c_size_t, []),
+        "wq_rmsnorm_dev": (ci, [ci, vp, ci, cl, vp, cl, vp, cf, ci, ci, vp, ci, cl, vp, vp, cl, vp]),
+        "wq_rope_create": (ci, [ci, ci, ctypes.c_double, _c_int_p, ci, ctypes.POINTER(vp)]),
+        "wq_rope_dev": (ci, [vp, ci, vp, ci, ci, ci, ci, cl, cl, vp, cl, vp, cl, cl, vp]),
+        "wq_rope_free": (ci, [vp]),
+        "wq_kv_append_dev": (ci, [cachep, batchp, vp, vp, ci, cl, cl, vp]),
+        "wq_kv_read_dev": (ci, [cachep, batchp, vp, vp, ci, cl, cl, vp]),
+        "wq_attn_paged_dev": (ci, [cachep, batchp, vp, ci, ci, cl, cl, cf, ci, ci, vp, cl, cl, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -376,3 +401,209 @@ def wq_stream_read_dev(buf_dev, waves: int, loads_in_flight: int, out_dev, strea
     _check(lib.wq_stream_read_dev(ctypes.c_void_p(buf_dev.data_ptr()), nbytes, int(waves), int(loads_in_flight),
                                   ctypes.c_void_p(out_dev.data_ptr()), _stream_handle(stream, buf_dev.device)),
            "wq_stream_read_dev")
+
+
+# ----------------------------------------------------------------------------
+# between a decoder layer's products: norm, rotary positions, cache, attention
+
+_DT = {} if torch is None else {torch.float32: WQ_DT_F32, torch.bfloat16: WQ_DT_BF16, torch.float16: WQ_DT_F16,
+                                torch.int8: WQ_DT_I8}
+
+
+def _dev(t, dims, what, dtypes=(WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16)):
+    """The type code of a GPU tensor with `dims` dimensions, the last one contiguous."""
+    if torch is None or not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor on a GPU" % what)
+    dt = _DT.get(t.dtype, -1)
+    if dt not in dtypes or not t.is_cuda:
+        raise ValueError("%s: a %s tensor on %s is not taken" % (what, t.dtype, t.device))
+    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError("%s must have %d dimensions, the last one contiguous" % (what, dims))
+    return dt
+
+
+def _like(t, ref, what, shape=None, dtype=None):
+    """t has the shape, type and device asked for (ref's own where not given)."""
+    if tuple(t.shape) != tuple(ref.shape if shape is None else shape):
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(ref.shape if shape is None else shape), tuple(t.shape)))
+    if t.dtype != (ref.dtype if dtype is None else dtype):
+        raise ValueError("%s must be %s, got %s" % (what, ref.dtype if dtype is None else dtype, t.dtype))
+    if t.device != ref.device:
+        raise ValueError("%s is on %s, expected %s" % (what, t.device, ref.device))
+
+
+def wq_rmsnorm_dev(x, w, eps: float, y, residual=None, sum_out=None, y_scale=None, stream=None) -> None:
+    """y[rows, n] = norm of x (+ residual) times w; sum_out receives x + residual in x's type.
+
+    y float32, bfloat16, float16, or int8 codes with y_scale [rows] (y ~ code * y_scale)."""
+    dt = _dev(x, 2, "x")
+    ydt = _dev(y, 2, "y", (WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16, WQ_DT_I8))
+    rows, n = x.shape
+    _like(y, x, "y", dtype=y.dtype)
+    _like(w, x, "w", (n,), torch.float32)
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    if (ydt == WQ_DT_I8) != (y_scale is not None):
+        raise ValueError("y_scale goes with an int8 y")
+    for t, what in ((residual, "residual"), (sum_out, "sum_out")):
+        if t is not None:
+            _like(t, x, what)
+            _dev(t, 2, what)
+    if y_scale is not None:
+        _like(y_scale, x, "y_scale", (rows,), torch.float32)
+        if not y_scale.is_contiguous():
+            raise ValueError("y_scale must be contiguous")
+    dev = x.device.index
+    _check(lib.wq_rmsnorm_dev(dev, x.data_ptr(), dt, x.stride(0), None if residual is None else residual.data_ptr(),
+                              0 if residual is None else residual.stride(0), w.data_ptr(), eps, rows, n, y.data_ptr(),
+                              ydt, y.stride(0), None if y_scale is None else y_scale.data_ptr(),
+                              None if sum_out is None else sum_out.data_ptr(),
+                              0 if sum_out is None else sum_out.stride(0), _stream_handle(stream, dev)),
+           "wq_rmsnorm_dev")
+
+
+class Rope:
+    """Plan of rotary positions (the C wq_rope*; host memory, released with the object or wq_rope_free)."""
+
+    def __init__(self, ptr: ctypes.c_void_p, rot: int, axes: int):
+        self.ptr, self.rot, self.axes = ptr, rot, axes
+
+    def __del__(self):
+        if self.ptr and lib is not None:
+            lib.wq_rope_free(self.ptr)
+            self.ptr = None
+
+
+def wq_rope_create(rot: int, pairing: int, theta: float, sections) -> Rope:
+    """Plan for heads whose first `rot` elements turn; sections[a] pairs follow axis a.
+
+    pairing 0 pairs element i with i + rot/2, pairing 1 element 2i with 2i + 1."""
+    sec = list(sections)
+    arr = (ctypes.c_int * max(1, len(sec)))(*sec)
+    h = ctypes.c_void_p(None)
+    _check(lib.wq_rope_create(int(rot), int(pairing), float(theta), arr, len(sec), ctypes.byref(h)), "wq_rope_create")
+    return Rope(h, int(rot), len(sec))
+
+
+def wq_rope_dev(rope: Rope, x, pos, y, stream=None) -> None:
+    """y[T, H, D] = x turned by the positions pos [axes, T] (int32); y may be x."""
+    dt = _dev(x, 3, "x")
+    _dev(y, 3, "y")
+    _like(y, x, "y")
+    T, H, D = x.shape
+    if pos.dtype != torch.int32 or tuple(pos.shape) != (rope.axes, T) or pos.device != x.device or (
+            T > 1 and pos.stride(1) != 1):
+        raise ValueError("pos must be int32 [%d, %d] on %s, contiguous along the tokens" % (rope.axes, T, x.device))
+    dev = x.device.index
+    xt, xh, _ = x.stride()
+    yt, yh, _ = y.stride()
+    _check(lib.wq_rope_dev(rope.ptr, dev, x.data_ptr(), dt, T, H, D, xt, xh, pos.data_ptr(), pos.stride(0),
+                           y.data_ptr(), yt, yh, _stream_handle(stream, dev)), "wq_rope_dev")
+
+
+def wq_rope_free(rope: Rope) -> None:
+    if rope is None:
+        return
+    _check(lib.wq_rope_free(rope.ptr), "wq_rope_free")
+    rope.ptr = None
+
+
+class KvCache:
+    """A paged, quantised key/value cache over the caller's pools.
+
+    k, v: uint8 [pages, heads, page, row bytes] with the same strides, rows contiguous; a row holds D float16 codes
+    (2 D bytes, WQ_KV_F16), D int8 codes (WQ_KV_I8) or two 4-bit codes a byte (D / 2 bytes, WQ_KV_I4).
+    k_scale, v_scale: float32 [pages, heads, page] with the same strides."""
+
+    def __init__(self, kind: int, k, v, k_scale, v_scale):
+        if kind not in (WQ_KV_F16, WQ_KV_I8, WQ_KV_I4):
+            raise ValueError("kind must be WQ_KV_F16, WQ_KV_I8 or WQ_KV_I4")
+        for t, what, dt, dims in ((k, "k", torch.uint8, 4), (v, "v", torch.uint8, 4),
+                                  (k_scale, "k_scale", torch.float32, 3), (v_scale, "v_scale", torch.float32, 3)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch tensor on a GPU" % what)
+            if t.dtype != dt or not t.is_cuda or t.dim() != dims or t.device != k.device:
+                raise ValueError("%s must be a %s tensor with %d dimensions, on k's GPU" % (what, dt, dims))
+        if k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same shape and strides, rows contiguous")
+        if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or k_scale.stride() != v_scale.stride():
+            raise ValueError("k_scale and v_scale must have the shape of k without its rows, and the same strides")
+        pages, heads, page, rb = k.shape
+        self.kind, self.dim, self.heads, self.page = kind, (rb // 2, rb, rb * 2)[kind], heads, page
+        self.tensors = (k, v, k_scale, v_scale)
+        self.device = k.device
+        self.c = _KvCacheC(k.device.index, kind, pages, heads, page, self.dim, k.data_ptr(), v.data_ptr(),
+                           k_scale.data_ptr(), v_scale.data_ptr(), (ctypes.c_long * 3)(*k.stride()[:3]),
+                           (ctypes.c_long * 3)(*k_scale.stride()))
+        self.ref = ctypes.byref(self.c)
+
+
+class KvBatch:
+    """The new tokens of B sequences: q_start int32 [B+1], kv_len int32 [B] (new tokens among them), table int32
+    [B, width] of pages, all on the GPU; T = q_start[B] tokens. max_q, max_kv: the longest lengths, if known."""
+
+    def __init__(self, q_start, kv_len, table, T: int, max_q: int = 0, max_kv: int = 0):
+        for t, what, dims in ((q_start, "q_start", 1), (kv_len, "kv_len", 1), (table, "table", 2)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch tensor on a GPU" % what)
+            if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims or t.device != q_start.device:
+                raise ValueError("%s must be an int32 GPU tensor with %d dimensions" % (what, dims))
+            if t.stride(-1) != 1 and t.shape[-1] > 1:
+                raise ValueError("%s must be contiguous" % what)
+        B, width = table.shape
+        if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
+            raise ValueError("q_start, kv_len and table must hold B + 1, B and B rows")
+        self.B, self.T, self.device = B, int(T), q_start.device
+        self.tensors = (q_start, kv_len, table)
+        self.c = _KvBatchC(B, self.T, width, int(max_q), int(max_kv), table.stride(0), q_start.data_ptr(),
+                           kv_len.data_ptr(), table.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+def _tokens(cache, batch, a, b, what):
+    """The type code of the tokens' keys and values a, b [T, heads, D]."""
+    dt = _dev(a, 3, what)
+    _dev(b, 3, what)
+    if a.shape != b.shape or a.dtype != b.dtype or a.stride() != b.stride():
+        raise ValueError("%s must have the same shape, type and strides" % what)
+    if tuple(a.shape) != (batch.T, cache.heads, cache.dim):
+        raise ValueError("%s must have shape %s" % (what, (batch.T, cache.heads, cache.dim)))
+    if not (a.device == b.device == cache.device == batch.device):
+        raise ValueError("%s, the cache and the batch must be on one GPU" % what)
+    return dt
+
+
+def wq_kv_append_dev(cache: KvCache, batch: KvBatch, k_new, v_new, stream=None) -> None:
+    """Quantise the batch's keys and values [T, heads, D] into their slots of the cache."""
+    dt = _tokens(cache, batch, k_new, v_new, "k_new and v_new")
+    st = k_new.stride()
+    _check(lib.wq_kv_append_dev(cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), dt, st[0], st[1],
+                                _stream_handle(stream, cache.device.index)), "wq_kv_append_dev")
+
+
+def wq_kv_read_dev(cache: KvCache, batch: KvBatch, k_out, v_out, stream=None) -> None:
+    """The values of the batch's tokens in the cache, into k_out, v_out [T, heads, D]."""
+    dt = _tokens(cache, batch, k_out, v_out, "k_out and v_out")
+    st = k_out.stride()
+    _check(lib.wq_kv_read_dev(cache.ref, batch.ref, k_out.data_ptr(), v_out.data_ptr(), dt, st[0], st[1],
+                              _stream_handle(stream, cache.device.index)), "wq_kv_read_dev")
+
+
+def wq_attn_paged_dev(cache: KvCache, batch: KvBatch, q, o, scale: float, causal: bool = True, window: int = 0,
+                      lse=None, stream=None) -> None:
+    """o[T, H, D] = attention of the batch's tokens q [T, H, D] over the cache; lse float32 [T, H] if given."""
+    dt = _dev(q, 3, "q")
+    _dev(o, 3, "o")
+    _like(o, q, "o")
+    T, H, D = q.shape
+    if T != batch.T or D != cache.dim or not (q.device == cache.device == batch.device):
+        raise ValueError("q must have shape [%d, H, %d] on %s" % (batch.T, cache.dim, cache.device))
+    if lse is not None:
+        _like(lse, q, "lse", (T, H), torch.float32)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    qt, qh, _ = q.stride()
+    ot, oh, _ = o.stride()
+    _check(lib.wq_attn_paged_dev(cache.ref, batch.ref, q.data_ptr(), dt, H, qt, qh, scale, int(causal), int(window),
+                                 o.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
+                                 _stream_handle(stream, cache.device.index)), "wq_attn_paged_dev")

@@ -1,0 +1,267 @@
+// C entry points of the operators between a decoder layer's products
+// (include/wqmm.h): argument checks and launches.
+#include <climits>
+#include <cmath>
+#include <new>
+
+#include "decoder.h"
+
+namespace {
+
+struct DeviceScope { // makes `dev` current, restoring the caller's device after
+    int prev = -1;
+    bool switched = false;
+    explicit DeviceScope(int dev) {
+        if (hipGetDevice(&prev) == hipSuccess && prev != dev) switched = hipSetDevice(dev) == hipSuccess;
+    }
+    ~DeviceScope() {
+        if (switched) (void)hipSetDevice(prev);
+    }
+};
+
+int status(hipError_t e) { return e == hipSuccess ? WQ_OK : e == hipErrorOutOfMemory ? WQ_E_OOM : WQ_E_HIP; }
+
+bool float_type(int t) { return t >= WQ_DT_F32 && t <= WQ_DT_F16; }
+
+int size_of(int t) { return t == WQ_DT_F32 ? 4 : t == WQ_DT_I8 ? 1 : 2; }
+
+bool aligned(const void *p, long a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
+
+// A buffer whose rows start at multiples of `a` bytes (strides in elements of `size` bytes).
+bool rows_aligned(const void *p, long s0, long s1, int size, long a) {
+    return aligned(p, a) && s0 * size % a == 0 && s1 * size % a == 0;
+}
+
+int check_cache(const wq_kv_cache *c) {
+    if (c == nullptr || c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr)
+        return WQ_E_INVAL;
+    if (c->kind < WQ_KV_F16 || c->kind > WQ_KV_I4 || c->pages <= 0 || c->heads <= 0 || c->page <= 0 || c->dim <= 0)
+        return WQ_E_INVAL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return WQ_E_INVAL;
+    for (int i = 0; i < 3; ++i)
+        if (c->row_stride[i] < 0 || c->row_stride[i] % 16 != 0 || c->scale_stride[i] < 0) return WQ_E_INVAL;
+    if ((c->dim != 64 && c->dim != 128 && c->dim != 256) || c->heads > WQ_KV_MAX_HEADS) return WQ_E_UNSUPPORTED;
+    return WQ_OK;
+}
+
+int check_batch(const wq_kv_batch *b) {
+    if (b == nullptr || b->B < 0 || b->T < 0 || b->width < 0 || b->max_q < 0 || b->max_kv < 0 || b->table_stride < 0)
+        return WQ_E_INVAL;
+    if (b->B == 0 && b->T > 0) return WQ_E_INVAL;
+    if (b->T == 0) return WQ_OK;
+    if (b->q_start == nullptr || b->kv_len == nullptr || (b->table == nullptr && b->width > 0)) return WQ_E_INVAL;
+    if (!aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->table, 4)) return WQ_E_INVAL;
+    return WQ_OK;
+}
+
+wq::KvView view(const wq_kv_cache *c) {
+    wq::KvView v;
+    v.k = (const uint8_t *)c->k;
+    v.v = (const uint8_t *)c->v;
+    v.ks = c->k_scale;
+    v.vs = c->v_scale;
+    v.rp = c->row_stride[0];
+    v.rh = c->row_stride[1];
+    v.rs = c->row_stride[2];
+    v.sp = c->scale_stride[0];
+    v.sh = c->scale_stride[1];
+    v.ss = c->scale_stride[2];
+    v.pages = c->pages;
+    v.heads = c->heads;
+    v.page = c->page;
+    return v;
+}
+
+wq::BatchView view(const wq_kv_batch *b) {
+    wq::BatchView v;
+    v.q_start = b->q_start;
+    v.kv_len = b->kv_len;
+    v.table = b->table;
+    v.table_stride = b->table_stride;
+    v.B = b->B;
+    v.T = b->T;
+    v.width = b->width;
+    return v;
+}
+
+int kv_copy(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k, void *v, int dtype, long tok, long head,
+            bool write, hipStream_t st) {
+    int rc = check_cache(cache);
+    if (rc == WQ_OK) rc = check_batch(batch);
+    if (rc != WQ_OK) return rc;
+    if (!float_type(dtype) || tok < 0 || head < 0) return WQ_E_INVAL;
+    if (batch->T == 0) return WQ_OK;
+    const int size = size_of(dtype);
+    if (k == nullptr || v == nullptr || !aligned(k, size) || !aligned(v, size)) return WQ_E_INVAL;
+    if ((rc = wq::begin_call(cache->device)) != WQ_OK) return rc;
+    if ((long)batch->T * 2 * cache->heads > (long)INT_MAX * 8) return WQ_E_UNSUPPORTED;
+    DeviceScope scope(cache->device);
+    wq::KvCopyArgs a;
+    a.c = view(cache);
+    a.b = view(batch);
+    a.k = k;
+    a.v = v;
+    a.tok = tok;
+    a.head = head;
+    const bool vec = rows_aligned(k, tok, head, size, 16) && aligned(v, 16);
+    return status(write ? wq::launch_kv_append(a, cache->kind, cache->dim, dtype, vec, st)
+                        : wq::launch_kv_read(a, cache->kind, cache->dim, dtype, vec, st));
+}
+
+} // namespace
+
+extern "C" {
+
+int wq_rmsnorm_dev(int device, const void *x, int x_dtype, long x_stride, const void *residual, long res_stride,
+                   const float *w, float eps, int rows, int n, void *y, int y_dtype, long y_stride, float *y_scale,
+                   void *sum_out, long sum_stride, void *hip_stream) {
+    if (!float_type(x_dtype) || (!float_type(y_dtype) && y_dtype != WQ_DT_I8)) return WQ_E_INVAL;
+    if (rows < 0 || n <= 0 || x_stride < 0 || y_stride < 0 || !(eps >= 0.f)) return WQ_E_INVAL;
+    if ((residual && res_stride < 0) || (sum_out && sum_stride < 0)) return WQ_E_INVAL;
+    if (n > WQ_NORM_MAX_N) return WQ_E_UNSUPPORTED;
+    if (rows == 0) return WQ_OK;
+    if (x == nullptr || w == nullptr || y == nullptr || (y_dtype == WQ_DT_I8) != (y_scale != nullptr)) return WQ_E_INVAL;
+    const int sx = size_of(x_dtype), sy = size_of(y_dtype);
+    if (!aligned(x, sx) || !aligned(residual, sx) || !aligned(sum_out, sx) || !aligned(y, sy) || !aligned(w, 4) ||
+        !aligned(y_scale, 4))
+        return WQ_E_INVAL;
+    const int rc = wq::begin_call(device);
+    if (rc != WQ_OK) return rc;
+    DeviceScope scope(device);
+    wq::NormArgs a;
+    a.x = x;
+    a.res = residual;
+    a.w = w;
+    a.y = y;
+    a.sum = sum_out;
+    a.y_scale = y_scale;
+    a.xs = x_stride;
+    a.rs = res_stride;
+    a.ys = y_stride;
+    a.ss = sum_stride;
+    a.eps = eps;
+    a.rows = rows;
+    a.n = n;
+    const int vec = 16 / sx; // elements of a wide load of x
+    const long ya = vec * sy < 16 ? vec * sy : 16;
+    const bool wide = n % vec == 0 && rows_aligned(x, x_stride, 0, sx, 16) && aligned(w, 16) &&
+                      rows_aligned(y, y_stride, 0, sy, ya) && (!residual || rows_aligned(residual, res_stride, 0, sx, 16)) &&
+                      (!sum_out || rows_aligned(sum_out, sum_stride, 0, sx, 16));
+    return status(wq::launch_rmsnorm(a, x_dtype, y_dtype, wide, wq::device_cus(device), (hipStream_t)hip_stream));
+}
+
+int wq_rope_create(int rot, int pairing, double theta, const int *sections, int axes, wq_rope **rope) {
+    if (rope == nullptr || sections == nullptr || rot <= 0 || rot % 2 != 0 || (pairing != 0 && pairing != 1) ||
+        axes <= 0 || !(theta > 0.0) || !std::isfinite(theta))
+        return WQ_E_INVAL;
+    if (rot > WQ_ROPE_MAX_ROT || axes > WQ_ROPE_MAX_AXES) return WQ_E_UNSUPPORTED;
+    long sum = 0;
+    for (int i = 0; i < axes; ++i) {
+        if (sections[i] < 0) return WQ_E_INVAL;
+        sum += sections[i];
+    }
+    if (sum != rot / 2) return WQ_E_INVAL;
+    wq_rope *r = new (std::nothrow) wq_rope;
+    if (r == nullptr) return WQ_E_OOM;
+    r->magic = kRopeMagic;
+    r->rot = rot;
+    r->pairing = pairing;
+    r->axes = axes;
+    int i = 0;
+    for (int ax = 0; ax < axes; ++ax)
+        for (int j = 0; j < sections[ax]; ++j, ++i) {
+            r->turns[i] = std::pow(theta, -2.0 * i / rot) / (2.0 * M_PI);
+            r->axis[i] = (uint8_t)ax;
+        }
+    *rope = r;
+    return WQ_OK;
+}
+
+int wq_rope_dev(const wq_rope *rope, int device, const void *x, int dtype, int T, int H, int D, long x_tok,
+                long x_head, const int *pos_dev, long pos_stride, void *y, long y_tok, long y_head, void *hip_stream) {
+    if (rope == nullptr || rope->magic != kRopeMagic || !float_type(dtype) || T < 0 || H < 0 || D < rope->rot ||
+        x_tok < 0 || x_head < 0 || y_tok < 0 || y_head < 0 || pos_stride < 0)
+        return WQ_E_INVAL;
+    if (D > 65536 || H > WQ_KV_MAX_HEADS) return WQ_E_UNSUPPORTED;
+    if (T == 0 || H == 0) return WQ_OK;
+    const int size = size_of(dtype);
+    if (x == nullptr || y == nullptr || pos_dev == nullptr || !aligned(x, size) || !aligned(y, size) ||
+        !aligned(pos_dev, 4))
+        return WQ_E_INVAL;
+    const int rc = wq::begin_call(device);
+    if (rc != WQ_OK) return rc;
+    DeviceScope scope(device);
+    wq::RopeArgs a;
+    a.x = x;
+    a.y = y;
+    a.pos = pos_dev;
+    a.pos_stride = pos_stride;
+    a.xt = x_tok;
+    a.xh = x_head;
+    a.yt = y_tok;
+    a.yh = y_head;
+    a.T = T;
+    a.H = H;
+    a.D = D;
+    a.rot = rope->rot;
+    a.pairing = rope->pairing;
+    for (int i = 0; i < rope->rot / 2; ++i) {
+        a.turns[i] = rope->turns[i];
+        a.axis[i] = rope->axis[i];
+    }
+    const bool vec = rows_aligned(x, x_tok, x_head, size, 16) && rows_aligned(y, y_tok, y_head, size, 16);
+    return status(wq::launch_rope(a, dtype, vec, wq::device_cus(device), (hipStream_t)hip_stream));
+}
+
+int wq_rope_free(wq_rope *rope) {
+    if (rope == nullptr) return WQ_OK;
+    if (rope->magic != kRopeMagic) return WQ_E_INVAL;
+    rope->magic = 0;
+    delete rope;
+    return WQ_OK;
+}
+
+int wq_kv_append_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *k_new, const void *v_new,
+                     int dtype, long tok, long head, void *hip_stream) {
+    return kv_copy(cache, batch, const_cast<void *>(k_new), const_cast<void *>(v_new), dtype, tok, head, true,
+                   (hipStream_t)hip_stream);
+}
+
+int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_out, void *v_out, int dtype, long tok,
+                   long head, void *hip_stream) {
+    return kv_copy(cache, batch, k_out, v_out, dtype, tok, head, false, (hipStream_t)hip_stream);
+}
+
+int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *q, int dtype, int H, long q_tok,
+                      long q_head, float scale, int causal, int window, void *o, long o_tok, long o_head, float *lse,
+                      void *hip_stream) {
+    int rc = check_cache(cache);
+    if (rc == WQ_OK) rc = check_batch(batch);
+    if (rc != WQ_OK) return rc;
+    if (!float_type(dtype) || H <= 0 || H % cache->heads != 0 || q_tok < 0 || q_head < 0 || o_tok < 0 || o_head < 0 ||
+        window < 0 || !std::isfinite(scale))
+        return WQ_E_INVAL;
+    if (H > WQ_KV_MAX_HEADS) return WQ_E_UNSUPPORTED;
+    if (batch->T == 0) return WQ_OK;
+    const int size = size_of(dtype);
+    if (q == nullptr || o == nullptr || !aligned(q, size) || !aligned(o, size) || !aligned(lse, 4)) return WQ_E_INVAL;
+    if ((rc = wq::begin_call(cache->device)) != WQ_OK) return rc;
+    DeviceScope scope(cache->device);
+    wq::AttnArgs a;
+    a.c = view(cache);
+    a.b = view(batch);
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    a.qt = q_tok;
+    a.qh = q_head;
+    a.ot = o_tok;
+    a.oh = o_head;
+    a.scale = scale;
+    a.H = H;
+    a.causal = causal != 0;
+    a.window = window;
+    return status(wq::launch_attn(a, cache->kind, cache->dim, dtype, (hipStream_t)hip_stream));
+}
+
+} // extern "C"

@@ -17,6 +17,7 @@
 #include <mutex>
 #include <new>
 
+#include "decoder.h"
 #include "skinny_group.h"
 #include "staging.h"
 #include "wq_internal.h"
@@ -404,6 +405,24 @@ int ensure_scratch(DeviceCtx &d, size_t xb, size_t yb) {
 }
 
 } // namespace
+
+namespace wq {
+
+int begin_call(int device) {
+    if (!device_open(device)) return WQ_E_NOTINIT;
+    return g_cfg.fault == 2 ? WQ_E_FAULT : WQ_OK;
+}
+
+int stream_workspace(int device, size_t bytes, hipStream_t st, void **out) {
+    uint16_t *p = nullptr;
+    const int rc = ensure_workspace(g_dev[device], bytes, st, &p);
+    *out = p;
+    return rc;
+}
+
+int device_cus(int device) { return g_dev[device].cus; }
+
+} // namespace wq
 
 extern "C" {
 
