@@ -1,0 +1,206 @@
+// What the attention kernels share: the rows of a tile and the positions they
+// see, how cache codes become f16 operands, and partial results.
+#pragma once
+
+#include "decoder.h"
+
+namespace wq {
+
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A tile: up to R rows of one sequence and key/value head, row r standing for
+// new token r / G and query head kvh * G + r % G.
+//
+// Sequence b owns the tile numbers floor(q_start[b] G / R) + b up to
+// floor(q_start[b+1] G / R) + b, at least as many as its rows need, so a
+// block finds its sequence by comparing every lane's sequence with the tile's
+// number, without a prefix sum and without knowing the lengths on the host.
+struct Tile {
+    int b, tok0, n, row0, rows; // sequence, its first token and token count, first row, rows here (0: no tile)
+    int kv;                     // positions, those past the table left out
+    int past;                   // kv_len - n: position of new token 0
+};
+
+__host__ __device__ inline long tile_count(long T, long G, long R, long B) { return T * G / R + B; }
+
+template <int R>
+__device__ __forceinline__ Tile find_tile(const BatchView &b, int page, int G, long id, int lane) {
+    int hit = -1;
+    for (int i0 = 0; i0 < b.B; i0 += 64) {
+        const int i = i0 + lane;
+        bool mine = false;
+        if (i < b.B) {
+            const long s0 = min(max(b.q_start[i], 0), b.T), s1 = min(max(b.q_start[i + 1], 0), b.T);
+            const long first = s0 * G / R + i, last = s1 * G / R + i;
+            mine = s1 > s0 && id >= first && id <= last;
+        }
+        const uint64_t m = __ballot(mine);
+        if (m) {
+            hit = i0 + __builtin_ctzll(m);
+            break;
+        }
+    }
+    Tile t;
+    t.rows = 0;
+    t.b = t.tok0 = t.n = t.row0 = t.kv = t.past = 0;
+    if (hit < 0) return t;
+    hit = __builtin_amdgcn_readfirstlane(hit);
+    const int s0 = min(max(b.q_start[hit], 0), b.T), s1 = min(max(b.q_start[hit + 1], 0), b.T);
+    const long row0 = (id - ((long)s0 * G / R + hit)) * R, all = (long)(s1 - s0) * G;
+    t.b = hit;
+    t.tok0 = s0;
+    t.n = s1 - s0;
+    t.row0 = (int)row0;
+    t.rows = row0 < all ? (int)min((long)R, all - row0) : 0;
+    const int kv = max(b.kv_len[hit], 0);
+    const long held = (long)b.width * page;
+    t.past = kv - t.n;
+    t.kv = kv < held ? kv : (int)held;
+    return t;
+}
+
+// Positions [lo, hi) that new token i sees.
+__device__ __forceinline__ void seen_range(const Tile &t, int i, int causal, int window, int *lo, int *hi) {
+    const long p = (long)t.past + i;
+    long h = t.kv, l = 0;
+    if (causal && p + 1 < h) h = p + 1;
+    if (window > 0 && p + 1 > window) l = p + 1 - window;
+    *hi = (int)(h < 0 ? 0 : h);
+    *lo = (int)(l > *hi ? *hi : l);
+}
+
+// Blocks of STEP positions that the rows of a tile see, and their split:
+// `per` blocks a split, so the split does not depend on what the host knows.
+struct Span {
+    int base, blocks, per, splits;
+};
+
+template <int STEP>
+__device__ __forceinline__ Span find_span(int lo, int hi, int least, int nsplit) {
+    Span s;
+    s.base = lo / STEP * STEP;
+    s.blocks = hi > lo ? (hi - s.base + STEP - 1) / STEP : 0;
+    s.per = max(least, (s.blocks + nsplit - 1) / nsplit);
+    s.splits = s.blocks == 0 ? 1 : (s.blocks + s.per - 1) / s.per;
+    return s;
+}
+
+// ---------------------------------------------------------------------------
+// Codes to matrix operands, exactly.
+//
+// To f16: a half 0x6400 + u is 1024 + u for u < 1024, so one and-or puts two
+// codes into halves and one packed add takes the offset off. The constants are
+// opaque registers, one scalar: with literals the and and the or are two
+// instructions (an instruction takes one scalar register and no literal here).
+struct OpenConst {
+    uint32_t m0, m1, magic;
+    __device__ __forceinline__ OpenConst() : m0(0x000f000fu), m1(0x00f000f0u), magic(0x64006400u) {
+        asm volatile("" : "+s"(m0));
+        asm volatile("" : "+s"(m1));
+        asm volatile("" : "+v"(magic));
+    }
+};
+
+__device__ __forceinline__ uint32_t pk_add(uint32_t a, float c) {
+    const f16x2 r = __builtin_bit_cast(f16x2, a) + f16x2{(f16)c, (f16)c};
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ uint32_t pk_fma(uint32_t a, float m, float c) {
+    const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, a), f16x2{(f16)m, (f16)m}, f16x2{(f16)c, (f16)c});
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Four int8 codes, in order: two registers of two halves.
+__device__ __forceinline__ void open_i8(uint32_t w, uint32_t *o) {
+    const uint32_t x = w ^ 0x80808080u; // code + 128
+    o[0] = pk_add(__builtin_amdgcn_perm(0x64646464u, x, 0x04010400u), -1152.f);
+    o[1] = pk_add(__builtin_amdgcn_perm(0x64646464u, x, 0x04030402u), -1152.f);
+}
+
+// The nibbles of two 16-bit halves: registers with nibble 0, 1, 2, 3 of both.
+__device__ __forceinline__ void open_i4(const OpenConst &k, uint32_t w, uint32_t *o) {
+    const uint32_t v = w >> 8;
+    o[0] = pk_add((w & k.m0) | k.magic, -1032.f);
+    o[1] = pk_fma((w & k.m1) | k.magic, 0.0625f, -72.f);
+    o[2] = pk_add((v & k.m0) | k.magic, -1032.f);
+    o[3] = pk_fma((v & k.m1) | k.magic, 0.0625f, -72.f);
+}
+
+// To bf16: a code in fp32 has its low 16 bits clear, so the upper halves of two
+// are the two bf16 values.
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
+// Byte k of w as a signed number (one conversion with its byte select).
+__device__ __forceinline__ float byte_i8(uint32_t w, int k) {
+    return (float)(int8_t)(w >> (8 * k));
+}
+
+// The low nibble of byte k of w, two's complement, times 1/16.
+__device__ __forceinline__ float nibble_i4(uint32_t w, int k) { return __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (8 * k) & 0xffu)); }
+
+// Element order of eight consecutive codes in a K operand.
+template <int KIND>
+__device__ __forceinline__ constexpr int k_order(int e) {
+    return KIND == WQ_KV_I4 ? (e >> 1) + 4 * (e & 1) : e;
+}
+
+__device__ __forceinline__ f16x8 join4(const uint32_t *r) {
+    const u32x4 v = {r[0], r[1], r[2], r[3]};
+    return __builtin_bit_cast(f16x8, v);
+}
+
+// Power of two that brings |x| <= top to below 2^14 (top itself into [2^13, 2^14)), as its exponent.
+__device__ __forceinline__ int head_room(float top) {
+    if (!(top < INFINITY)) return 0; // a row with an infinity or a NaN has no result
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    return 13 - max(e, -100);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// A pair of floats as three bf16 pairs that sum to them exactly (24 bits).
+__device__ __forceinline__ void split3(float a, float b, uint32_t *o) {
+    o[0] = high_halves(a, b);
+    a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+    b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+    o[1] = high_halves(a, b);
+    a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+    b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+    o[2] = high_halves(a, b);
+}
+
+// Two floats rounded to halves (to nearest), in one register.
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+// ---------------------------------------------------------------------------
+struct AttnPlan {
+    int few_tiles;  // 16-row tiles a wave carries (few-rows kernel)
+    int nsplit;     // most splits of a tile's positions
+    int least;      // fewest blocks of positions a split takes
+    long tiles;     // tile numbers
+    size_t ws_bytes;
+};
+
+// Partial results of a split: row (token, head) and split s at part[(row * nsplit + s) * D], their maximum
+// (base 2) and sum at ml[(row * nsplit + s) * 2].
+struct Partials {
+    float *part, *ml;
+    int nsplit, least;
+};
+
+} // namespace wq

@@ -56,6 +56,9 @@ struct KvView {
     long rp, rh, rs; // row strides: page, head, slot (bytes)
     long sp, sh, ss; // scale strides (floats)
     int pages, heads, page;
+    // position / page = mulhi(position, page_mul) >> page_shift; page_mul 0: a page of one position
+    uint32_t page_mul;
+    int page_shift;
 };
 
 struct BatchView {
@@ -83,7 +86,10 @@ struct AttnArgs {
     float scale;
     int H, causal, window;
 };
-hipError_t launch_attn(const AttnArgs &a, int kind, int dim, int dtype, hipStream_t st);
+struct AttnPlan;
+struct Partials;
+hipError_t launch_attn_few(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int kind, int dim, int dtype, bool vec,
+                           bool wide, hipStream_t st);
 
 } // namespace wq
 
@@ -124,10 +130,15 @@ __device__ __forceinline__ int sequence_of(const int *q_start, int B, int tok, i
     return n;
 }
 
+// Position / page, for positions below 2^31.
+__device__ __forceinline__ int page_index(const KvView &c, int t) {
+    return c.page_mul ? (int)(__umulhi((uint32_t)t, c.page_mul) >> c.page_shift) : t;
+}
+
 // Row of position t of sequence b: false if it is not there.
 __device__ __forceinline__ bool find_row(const KvView &c, const BatchView &b, int seq, long t, int *page, int *slot) {
     if (t < 0) return false;
-    const int i = (int)((unsigned)t / (unsigned)c.page);
+    const int i = page_index(c, (int)t);
     if (i >= b.width) return false;
     const int pg = b.table[(long)seq * b.table_stride + i];
     *page = pg;

@@ -4,7 +4,7 @@
 #include <cmath>
 #include <new>
 
-#include "decoder.h"
+#include "attn_common.h"
 
 namespace {
 
@@ -69,6 +69,11 @@ wq::KvView view(const wq_kv_cache *c) {
     v.pages = c->pages;
     v.heads = c->heads;
     v.page = c->page;
+    // floor(2^(31+L) / page) + 1 with page <= 2^L: exact for positions below 2^31
+    int L = 0;
+    while ((1L << L) < c->page) ++L;
+    v.page_mul = L == 0 ? 0 : (uint32_t)((1ull << (31 + L)) / (unsigned)c->page + 1);
+    v.page_shift = L - 1;
     return v;
 }
 
@@ -106,6 +111,38 @@ int kv_copy(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k, void *v
     const bool vec = rows_aligned(k, tok, head, size, 16) && aligned(v, 16);
     return status(write ? wq::launch_kv_append(a, cache->kind, cache->dim, dtype, vec, st)
                         : wq::launch_kv_read(a, cache->kind, cache->dim, dtype, vec, st));
+}
+
+// How the positions are split: enough waves for every SIMD to have some in
+// flight, but no split shorter than pays for its partial result. Lengths that
+// are not known are taken from the table's width.
+wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int causal, int window, int cus) {
+    wq::AttnPlan p;
+    const long G = H / c->heads;
+    const long q = b->max_q > 0 ? (b->max_q < b->T ? b->max_q : b->T) : ((long)b->T + b->B - 1) / b->B;
+    long kv = (long)b->width * c->page;
+    if (b->max_kv > 0 && b->max_kv < kv) kv = b->max_kv;
+    if (window > 0 && causal && (long)window + q < kv) kv = (long)window + q;
+    const int row = c->kind == WQ_KV_F16 ? 2 * c->dim : c->kind == WQ_KV_I8 ? c->dim : c->dim / 2;
+    const int step = row <= 128 ? 64 : 32;
+    p.few_tiles = q * G > 16 && c->dim <= 128 ? 2 : 1;
+    const long R = 16 * p.few_tiles;
+    p.tiles = wq::tile_count(b->T, G, R, b->B);
+    // tiles that are there: the numbers left unused by whole sequences not counted
+    const long full = (q * G + R - 1) / R * b->B;
+    const long blocks = (kv + step - 1) / step + 1;
+    const long total = (full < p.tiles ? full : p.tiles) * c->heads * blocks;
+    long per_wave = total / (cus * 12);
+    per_wave = per_wave < 1 ? 1 : per_wave > 8 ? 8 : per_wave;
+    p.least = (int)(4 * per_wave);
+    long n = (blocks + p.least - 1) / p.least;
+    const long rows = (long)b->T * H;
+    const long cap = (256L << 20) / (rows * (c->dim + 2) * 4); // workspace of at most 256 MiB
+    n = n > 512 ? 512 : n;
+    n = n > cap ? cap : n;
+    p.nsplit = (int)(n < 1 ? 1 : n);
+    p.ws_bytes = p.nsplit > 1 ? (size_t)rows * p.nsplit * (c->dim + 2) * 4 : 0;
+    return p;
 }
 
 } // namespace
@@ -261,7 +298,25 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
     a.H = H;
     a.causal = causal != 0;
     a.window = window;
-    return status(wq::launch_attn(a, cache->kind, cache->dim, dtype, (hipStream_t)hip_stream));
+    const wq::AttnPlan p = plan_attn(cache, batch, H, a.causal, window, wq::device_cus(cache->device));
+    wq::Partials pt;
+    pt.part = pt.ml = nullptr;
+    pt.nsplit = p.nsplit;
+    pt.least = p.least;
+    if (p.ws_bytes > 0) {
+        void *ws = nullptr;
+        if ((rc = wq::stream_workspace(cache->device, p.ws_bytes, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
+        pt.part = (float *)ws;
+        pt.ml = pt.part + (size_t)batch->T * H * p.nsplit * cache->dim;
+    }
+    const bool vec = rows_aligned(q, q_tok, q_head, size, 16) && rows_aligned(o, o_tok, o_head, size, 16);
+    // pools whose rows and scales all lie within 2^32 bytes are addressed by 32-bit offsets
+    const auto extent = [&](const long *s) {
+        return (double)(cache->pages - 1) * s[0] + (double)(cache->heads - 1) * s[1] + (double)(cache->page - 1) * s[2];
+    };
+    const bool wide = extent(cache->row_stride) + 2 * cache->dim >= 4294967296.0 ||
+                      4 * (extent(cache->scale_stride) + 1) >= 4294967296.0;
+    return status(wq::launch_attn_few(a, p, pt, cache->kind, cache->dim, dtype, vec, wide, (hipStream_t)hip_stream));
 }
 
 } // extern "C"
