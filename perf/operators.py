@@ -173,6 +173,8 @@ def prepare(case, seed):
         s["res"] = (randn(rows, n) * 2).to(dt) if c["res"] else None
         s["w"] = 1 + 0.2 * randn(n)
         if own:
+            import weight_only_quantized_matmul_amd as wq
+            wq.wq_init([0])
             out = torch.int8 if c["out"] == "i8" else DTYPES[c["out"]]
             s["y"] = torch.empty((rows, n), dtype=out, device="cuda")
             s["scale"] = torch.empty(rows, device="cuda") if c["out"] == "i8" else None
