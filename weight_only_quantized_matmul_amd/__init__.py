@@ -406,60 +406,65 @@ def wq_stream_read_dev(buf_dev, waves: int, loads_in_flight: int, out_dev, strea
 # ----------------------------------------------------------------------------
 # between a decoder layer's products: norm, rotary positions, cache, attention
 
-_DT = {} if torch is None else {torch.float32: WQ_DT_F32, torch.bfloat16: WQ_DT_BF16, torch.float16: WQ_DT_F16,
-                                torch.int8: WQ_DT_I8}
+_FLOATS = {} if torch is None else {torch.float32: WQ_DT_F32, torch.bfloat16: WQ_DT_BF16, torch.float16: WQ_DT_F16}
+_OUTS = {} if torch is None else {torch.int8: WQ_DT_I8, **_FLOATS}
+
+# The calls of one token's step are shorter than their checks if those are not kept lean: a tensor is checked once,
+# in one condition, and the message is made only when it fails.
 
 
-def _dev(t, dims, what, dtypes=(WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16)):
-    """The type code of a GPU tensor with `dims` dimensions, the last one contiguous."""
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _first(t, dims, types, what):
+    """(shape, type code, device, strides) of a GPU tensor with `dims` dimensions, the last one contiguous."""
     if torch is None or not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor on a GPU" % what)
-    dt = _DT.get(t.dtype, -1)
-    if dt not in dtypes or not t.is_cuda:
-        raise ValueError("%s: a %s tensor on %s is not taken" % (what, t.dtype, t.device))
-    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError("%s must have %d dimensions, the last one contiguous" % (what, dims))
-    return dt
+    dt = types.get(t.dtype, -1)
+    shape, st, dev = t.shape, t.stride(), t.get_device()
+    if dt < 0 or dev < 0 or len(shape) != dims or (st[-1] != 1 and shape[-1] > 1):
+        raise ValueError("%s: a %s tensor of shape %s and strides %s on %s is not taken" % (what, t.dtype, tuple(shape), st, t.device))
+    return shape, dt, dev, st
 
 
-def _like(t, ref, what, shape=None, dtype=None):
-    """t has the shape, type and device asked for (ref's own where not given)."""
-    if tuple(t.shape) != tuple(ref.shape if shape is None else shape):
-        raise ValueError("%s must have shape %s, got %s" % (what, tuple(ref.shape if shape is None else shape), tuple(t.shape)))
-    if t.dtype != (ref.dtype if dtype is None else dtype):
-        raise ValueError("%s must be %s, got %s" % (what, ref.dtype if dtype is None else dtype, t.dtype))
-    if t.device != ref.device:
-        raise ValueError("%s is on %s, expected %s" % (what, t.device, ref.device))
+def _more(t, shape, dtype, dev, what):
+    """The strides of a further tensor, with the shape, type and device asked for and its last dimension contiguous."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        st = t.stride()
+        if st[-1] == 1 or shape[-1] <= 1:
+            return st
+    raise ValueError("%s must be %s of shape %s on GPU %d, its last dimension contiguous; got %s, %s, %s" % (
+        what, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
 
 
 def wq_rmsnorm_dev(x, w, eps: float, y, residual=None, sum_out=None, y_scale=None, stream=None) -> None:
     """y[rows, n] = norm of x (+ residual) times w; sum_out receives x + residual in x's type.
 
     y float32, bfloat16, float16, or int8 codes with y_scale [rows] (y ~ code * y_scale)."""
-    dt = _dev(x, 2, "x")
-    ydt = _dev(y, 2, "y", (WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16, WQ_DT_I8))
-    rows, n = x.shape
-    _like(y, x, "y", dtype=y.dtype)
-    _like(w, x, "w", (n,), torch.float32)
-    if not w.is_contiguous():
-        raise ValueError("w must be contiguous")
+    shape, dt, dev, xs = _first(x, 2, _FLOATS, "x")
+    rows, n = shape
+    ydt = _OUTS.get(y.dtype, -1)
+    ys = _more(y, shape, y.dtype, dev, "y")
+    _more(w, shape[1:], torch.float32, dev, "w")
+    rp = rs = sp = ss = yp = None
+    if residual is not None:
+        rs = _more(residual, shape, x.dtype, dev, "residual")[0]
+        rp = residual.data_ptr()
+    if sum_out is not None:
+        ss = _more(sum_out, shape, x.dtype, dev, "sum_out")[0]
+        sp = sum_out.data_ptr()
     if (ydt == WQ_DT_I8) != (y_scale is not None):
         raise ValueError("y_scale goes with an int8 y")
-    for t, what in ((residual, "residual"), (sum_out, "sum_out")):
-        if t is not None:
-            _like(t, x, what)
-            _dev(t, 2, what)
     if y_scale is not None:
-        _like(y_scale, x, "y_scale", (rows,), torch.float32)
-        if not y_scale.is_contiguous():
-            raise ValueError("y_scale must be contiguous")
-    dev = x.device.index
-    _check(lib.wq_rmsnorm_dev(dev, x.data_ptr(), dt, x.stride(0), None if residual is None else residual.data_ptr(),
-                              0 if residual is None else residual.stride(0), w.data_ptr(), eps, rows, n, y.data_ptr(),
-                              ydt, y.stride(0), None if y_scale is None else y_scale.data_ptr(),
-                              None if sum_out is None else sum_out.data_ptr(),
-                              0 if sum_out is None else sum_out.stride(0), _stream_handle(stream, dev)),
-           "wq_rmsnorm_dev")
+        _more(y_scale, shape[:1], torch.float32, dev, "y_scale")
+        yp = y_scale.data_ptr()
+    rc = lib.wq_rmsnorm_dev(dev, x.data_ptr(), dt, xs[0], rp, rs or 0, w.data_ptr(), eps, rows, n, y.data_ptr(), ydt,
+                            ys[0], yp, sp, ss or 0, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_rmsnorm_dev")
 
 
 class Rope:
@@ -487,18 +492,14 @@ def wq_rope_create(rot: int, pairing: int, theta: float, sections) -> Rope:
 
 def wq_rope_dev(rope: Rope, x, pos, y, stream=None) -> None:
     """y[T, H, D] = x turned by the positions pos [axes, T] (int32); y may be x."""
-    dt = _dev(x, 3, "x")
-    _dev(y, 3, "y")
-    _like(y, x, "y")
-    T, H, D = x.shape
-    if pos.dtype != torch.int32 or tuple(pos.shape) != (rope.axes, T) or pos.device != x.device or (
-            T > 1 and pos.stride(1) != 1):
-        raise ValueError("pos must be int32 [%d, %d] on %s, contiguous along the tokens" % (rope.axes, T, x.device))
-    dev = x.device.index
-    xt, xh, _ = x.stride()
-    yt, yh, _ = y.stride()
-    _check(lib.wq_rope_dev(rope.ptr, dev, x.data_ptr(), dt, T, H, D, xt, xh, pos.data_ptr(), pos.stride(0),
-                           y.data_ptr(), yt, yh, _stream_handle(stream, dev)), "wq_rope_dev")
+    shape, dt, dev, xs = _first(x, 3, _FLOATS, "x")
+    ys = _more(y, shape, x.dtype, dev, "y")
+    T, H, D = shape
+    ps = _more(pos, (rope.axes, T), torch.int32, dev, "pos")
+    rc = lib.wq_rope_dev(rope.ptr, dev, x.data_ptr(), dt, T, H, D, xs[0], xs[1], pos.data_ptr(), ps[0], y.data_ptr(),
+                         ys[0], ys[1], _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_rope_dev")
 
 
 def wq_rope_free(rope: Rope) -> None:
@@ -531,7 +532,7 @@ class KvCache:
         pages, heads, page, rb = k.shape
         self.kind, self.dim, self.heads, self.page = kind, (rb // 2, rb, rb * 2)[kind], heads, page
         self.tensors = (k, v, k_scale, v_scale)
-        self.device = k.device
+        self.device, self.dev = k.device, k.get_device()
         self.c = _KvCacheC(k.device.index, kind, pages, heads, page, self.dim, k.data_ptr(), v.data_ptr(),
                            k_scale.data_ptr(), v_scale.data_ptr(), (ctypes.c_long * 3)(*k.stride()[:3]),
                            (ctypes.c_long * 3)(*k_scale.stride()))
@@ -553,7 +554,7 @@ class KvBatch:
         B, width = table.shape
         if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
             raise ValueError("q_start, kv_len and table must hold B + 1, B and B rows")
-        self.B, self.T, self.device = B, int(T), q_start.device
+        self.B, self.T, self.device, self.dev = B, int(T), q_start.device, q_start.get_device()
         self.tensors = (q_start, kv_len, table)
         self.c = _KvBatchC(B, self.T, width, int(max_q), int(max_kv), table.stride(0), q_start.data_ptr(),
                            kv_len.data_ptr(), table.data_ptr())
@@ -561,49 +562,47 @@ class KvBatch:
 
 
 def _tokens(cache, batch, a, b, what):
-    """The type code of the tokens' keys and values a, b [T, heads, D]."""
-    dt = _dev(a, 3, what)
-    _dev(b, 3, what)
-    if a.shape != b.shape or a.dtype != b.dtype or a.stride() != b.stride():
-        raise ValueError("%s must have the same shape, type and strides" % what)
-    if tuple(a.shape) != (batch.T, cache.heads, cache.dim):
-        raise ValueError("%s must have shape %s" % (what, (batch.T, cache.heads, cache.dim)))
-    if not (a.device == b.device == cache.device == batch.device):
-        raise ValueError("%s, the cache and the batch must be on one GPU" % what)
-    return dt
+    """(type code, strides) of the tokens' keys and values a, b [T, heads, D]."""
+    shape, dt, dev, st = _first(a, 3, _FLOATS, what)
+    if shape != (batch.T, cache.heads, cache.dim) or dev != cache.dev or dev != batch.dev:
+        raise ValueError("%s must have shape %s, on the GPU of the cache and the batch" % (what, (batch.T, cache.heads, cache.dim)))
+    if _more(b, shape, a.dtype, dev, what) != st:
+        raise ValueError("%s must have the same strides" % what)
+    return dt, st
 
 
 def wq_kv_append_dev(cache: KvCache, batch: KvBatch, k_new, v_new, stream=None) -> None:
     """Quantise the batch's keys and values [T, heads, D] into their slots of the cache."""
-    dt = _tokens(cache, batch, k_new, v_new, "k_new and v_new")
-    st = k_new.stride()
-    _check(lib.wq_kv_append_dev(cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), dt, st[0], st[1],
-                                _stream_handle(stream, cache.device.index)), "wq_kv_append_dev")
+    dt, st = _tokens(cache, batch, k_new, v_new, "k_new and v_new")
+    rc = lib.wq_kv_append_dev(cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), dt, st[0], st[1],
+                              _raw_stream(stream, cache.dev))
+    if rc:
+        _check(rc, "wq_kv_append_dev")
 
 
 def wq_kv_read_dev(cache: KvCache, batch: KvBatch, k_out, v_out, stream=None) -> None:
     """The values of the batch's tokens in the cache, into k_out, v_out [T, heads, D]."""
-    dt = _tokens(cache, batch, k_out, v_out, "k_out and v_out")
-    st = k_out.stride()
-    _check(lib.wq_kv_read_dev(cache.ref, batch.ref, k_out.data_ptr(), v_out.data_ptr(), dt, st[0], st[1],
-                              _stream_handle(stream, cache.device.index)), "wq_kv_read_dev")
+    dt, st = _tokens(cache, batch, k_out, v_out, "k_out and v_out")
+    rc = lib.wq_kv_read_dev(cache.ref, batch.ref, k_out.data_ptr(), v_out.data_ptr(), dt, st[0], st[1],
+                            _raw_stream(stream, cache.dev))
+    if rc:
+        _check(rc, "wq_kv_read_dev")
 
 
 def wq_attn_paged_dev(cache: KvCache, batch: KvBatch, q, o, scale: float, causal: bool = True, window: int = 0,
                       lse=None, stream=None) -> None:
     """o[T, H, D] = attention of the batch's tokens q [T, H, D] over the cache; lse float32 [T, H] if given."""
-    dt = _dev(q, 3, "q")
-    _dev(o, 3, "o")
-    _like(o, q, "o")
-    T, H, D = q.shape
-    if T != batch.T or D != cache.dim or not (q.device == cache.device == batch.device):
+    shape, dt, dev, qs = _first(q, 3, _FLOATS, "q")
+    os_ = _more(o, shape, q.dtype, dev, "o")
+    T, H, D = shape
+    if T != batch.T or D != cache.dim or dev != cache.dev or dev != batch.dev:
         raise ValueError("q must have shape [%d, H, %d] on %s" % (batch.T, cache.dim, cache.device))
+    lp = None
     if lse is not None:
-        _like(lse, q, "lse", (T, H), torch.float32)
-        if not lse.is_contiguous():
+        if _more(lse, shape[:2], torch.float32, dev, "lse")[0] != H and T > 1:
             raise ValueError("lse must be contiguous")
-    qt, qh, _ = q.stride()
-    ot, oh, _ = o.stride()
-    _check(lib.wq_attn_paged_dev(cache.ref, batch.ref, q.data_ptr(), dt, H, qt, qh, scale, int(causal), int(window),
-                                 o.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
-                                 _stream_handle(stream, cache.device.index)), "wq_attn_paged_dev")
+        lp = lse.data_ptr()
+    rc = lib.wq_attn_paged_dev(cache.ref, batch.ref, q.data_ptr(), dt, H, qs[0], qs[1], scale, 1 if causal else 0, window,
+                               o.data_ptr(), os_[0], os_[1], lp, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_attn_paged_dev")

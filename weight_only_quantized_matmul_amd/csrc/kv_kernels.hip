@@ -1,9 +1,10 @@
 // Quantising a key/value cache as it is written, and reading it back.
 //
-// D / 8 lanes take one row of one token, head and pool side, 8 elements a
-// lane: a wide load, the row's maximum over the lane group, 8 codes back in
-// one store. Both directions move every byte once and are bound by HBM (few
-// tokens: by the chain q_start -> kv_len -> table -> store).
+// D / 8 lanes take RPG rows of one token (keys and values of its heads), 8
+// elements a lane and row: a wide load, the row's maximum over the lane group,
+// 8 codes back in one store. Where the token lies is found once for its RPG
+// rows. Both directions move every byte once and are bound by HBM (few tokens:
+// by the chain q_start -> kv_len -> table -> row).
 #include "decoder.h"
 
 namespace wq {
@@ -37,145 +38,169 @@ __device__ __forceinline__ void store8(T *p, const float *v) {
     }
 }
 
-// What a lane group works on: token, side (0 keys, 1 values), head.
+// What a lane group works on: a token and its rows first .. first + RPG - 1,
+// keys of all heads before values of all heads.
 struct Where {
-    int tok, side, head;
-    bool any, there; // a row of the tokens' side; one of the cache too
-    long row, scale; // offsets in the pools (bytes, floats)
+    int tok, first;
+    bool any, there; // the token is one of the batch's; it has a place in the cache
+    long row, scale; // the place's offsets in the pools for head 0 (bytes, floats)
 };
 
-template <int LANES>
+template <int LANES, int RPG>
 __device__ __forceinline__ Where locate(const KvCopyArgs &a, int lane) {
     Where w;
-    const long r = ((long)blockIdx.x * kThreads + threadIdx.x) / LANES;
-    const int per = 2 * a.c.heads;
-    w.any = r < (long)a.b.T * per;
-    const long tok = w.any ? r / per : 0;
-    const int s = w.any ? (int)(r - tok * per) : 0;
-    w.tok = (int)tok;
-    w.side = s >= a.c.heads;
-    w.head = s - w.side * a.c.heads;
+    const unsigned parts = (2 * a.c.heads + RPG - 1) / RPG;
+    const unsigned r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const unsigned tok = r / parts;
+    w.any = tok < (unsigned)a.b.T;
+    w.tok = w.any ? (int)tok : 0;
+    w.first = (int)(r - tok * parts) * RPG;
     const int b = sequence_of<LANES>(a.b.q_start, a.b.B, w.tok, lane);
     w.there = false;
     w.row = w.scale = 0;
     if (w.any && b < a.b.B) {
         const int first = a.b.q_start[b], next = a.b.q_start[b + 1];
-        if (first <= w.tok && w.tok < next) {
-            const long t = (long)a.b.kv_len[b] - next + w.tok;
-            int page, slot;
-            if (find_row(a.c, a.b, b, t, &page, &slot)) {
-                w.there = true;
-                w.row = page * a.c.rp + w.head * a.c.rh + slot * a.c.rs;
-                w.scale = page * a.c.sp + w.head * a.c.sh + slot * a.c.ss;
-            }
+        const long t = (long)a.b.kv_len[b] - next + w.tok;
+        int page, slot;
+        if (first <= w.tok && w.tok < next && find_row(a.c, a.b, b, t, &page, &slot)) {
+            w.there = true;
+            w.row = page * a.c.rp + slot * a.c.rs;
+            w.scale = page * a.c.sp + slot * a.c.ss;
         }
     }
     return w;
 }
 
-template <typename T, int KIND, int D, bool VEC>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvCopyArgs a) {
-    constexpr int LANES = D / 8;
-    const int lane = threadIdx.x & (LANES - 1);
-    const Where w = locate<LANES>(a, lane);
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (w.there) load8<T, VEC>((const T *)(w.side ? a.v : a.k) + (long)w.tok * a.tok + (long)w.head * a.head + 8 * lane, v);
-    float top = 0.f;
-    bool bad = false;
+// The largest over a group of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, fabsf(v[i]));
-        bad = bad || !(fabsf(v[i]) < INFINITY);
-    }
-    int nb = bad ? 1 : 0;
-#pragma unroll
-    for (int m = LANES / 2; m > 0; m >>= 1) {
-        top = fmaxf(top, __shfl_xor(top, m));
-        nb |= __shfl_xor(nb, m);
-    }
-    if (!w.there) return;
-    uint8_t *row = const_cast<uint8_t *>(w.side ? a.c.v : a.c.k) + w.row + (long)lane * Codes<KIND>::bytes;
-    float scale;
-    const bool zero = nb || top < kTiny;
-    if constexpr (KIND == WQ_KV_F16) {
-        const int e = ilogbf(top) - 14;
-        scale = ldexpf(1.0f, e);
-        typedef f16 f16x8 __attribute__((ext_vector_type(8)));
-        f16x8 c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = zero ? (f16)0.f : (f16)ldexpf(v[i], -e); // exact but for the half's own rounding
-        *reinterpret_cast<f16x8 *>(row) = c;
-    } else {
-        constexpr int N = KIND == WQ_KV_I8 ? 127 : 7;
-        scale = (float)((double)top / N);
-        const float inv = 1.0f / scale;
-        int c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = v[i] * inv; // within N * 3 * 2^-24 of the quotient
-            float q = rintf(f);
-            if (fabsf(f - q) > 0.4999f) q = (float)rint((double)v[i] / (double)scale); // next to a border
-            c[i] = zero ? 0 : (int)q;
-        }
-        if constexpr (KIND == WQ_KV_I8) {
-            uint32_t u[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                u[j] = (c[4 * j] & 255) | (c[4 * j + 1] & 255) << 8 | (c[4 * j + 2] & 255) << 16 | (uint32_t)c[4 * j + 3] << 24;
-            *reinterpret_cast<uint2 *>(row) = make_uint2(u[0], u[1]);
-        } else {
-            uint32_t u = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u |= (uint32_t)(c[i] + 8) << (4 * i);
-            *reinterpret_cast<uint32_t *>(row) = u;
-        }
-    }
-    if (lane == 0) const_cast<float *>(w.side ? a.c.vs : a.c.ks)[w.scale] = nb ? NAN : zero ? 0.f : scale;
+    for (int m = LANES / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+    return v;
 }
 
-template <typename T, int KIND, int D, bool VEC>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(const KvCopyArgs a) {
+template <typename T, int KIND, int D, bool VEC, int RPG>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvCopyArgs a) {
     constexpr int LANES = D / 8;
-    const int lane = threadIdx.x & (LANES - 1);
-    const Where w = locate<LANES>(a, lane);
-    if (!w.any) return;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (w.there) {
-        const uint8_t *row = (w.side ? a.c.v : a.c.k) + w.row + (long)lane * Codes<KIND>::bytes;
-        const float scale = (w.side ? a.c.vs : a.c.ks)[w.scale];
-        if constexpr (KIND == WQ_KV_F16) {
-            load_vec<f16, 8>((const f16 *)row, v);
-        } else if constexpr (KIND == WQ_KV_I8) {
-            load_vec<int8_t, 8>((const int8_t *)row, v);
-        } else {
-            const uint32_t u = *reinterpret_cast<const uint32_t *>(row);
+    const int lane = threadIdx.x & (LANES - 1), H = a.c.heads;
+    const Where w = locate<LANES, RPG>(a, lane);
+    float v[RPG][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = (float)((int)(u >> (4 * i) & 15) - 8);
-        }
+    for (int j = 0; j < RPG; ++j) {
+        const int s = w.first + j, side = s >= H;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= scale;
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+        if (w.there && s < 2 * H)
+            load8<T, VEC>((const T *)(side ? a.v : a.k) + (long)w.tok * a.tok + (long)(s - side * H) * a.head + 8 * lane, v[j]);
     }
-    store8<T, VEC>((T *)(w.side ? a.v : a.k) + (long)w.tok * a.tok + (long)w.head * a.head + 8 * lane, v);
+#pragma unroll
+    for (int j = 0; j < RPG; ++j) {
+        const int s = w.first + j, side = s >= H, head = s - side * H;
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[j][i]));
+        // a NaN is not seen by the maximum: its lane hands on an infinity
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) nan = nan || v[j][i] != v[j][i];
+        top = group_max<LANES>(nan ? INFINITY : top);
+        if (!w.there || s >= 2 * H) continue;
+        uint8_t *row = const_cast<uint8_t *>(side ? a.c.v : a.c.k) + w.row + head * a.c.rh + (long)lane * Codes<KIND>::bytes;
+        const bool bad = !(top < INFINITY), zero = bad || top < kTiny;
+        float scale;
+        if constexpr (KIND == WQ_KV_F16) {
+            typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+            const int e = ilogbf(top) - 14;
+            scale = ldexpf(1.0f, e);
+            f16x8 c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = zero ? (f16)0.f : (f16)ldexpf(v[j][i], -e); // exact but for the half's own rounding
+            *reinterpret_cast<f16x8 *>(row) = c;
+        } else {
+            constexpr int N = KIND == WQ_KV_I8 ? 127 : 7;
+            scale = (float)((double)top / N);
+            const float inv = 1.0f / scale;
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = v[j][i] * inv; // within N * 3 * 2^-24 of the quotient
+                float q = rintf(f);
+                if (fabsf(f - q) > 0.4999f) q = (float)rint((double)v[j][i] / (double)scale); // next to a border
+                c[i] = zero ? 0 : (int)q;
+            }
+            if constexpr (KIND == WQ_KV_I8) {
+                uint32_t u[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    u[k] = (c[4 * k] & 255) | (c[4 * k + 1] & 255) << 8 | (c[4 * k + 2] & 255) << 16 | (uint32_t)c[4 * k + 3] << 24;
+                *reinterpret_cast<uint2 *>(row) = make_uint2(u[0], u[1]);
+            } else {
+                uint32_t u = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u |= (uint32_t)(c[i] + 8) << (4 * i);
+                *reinterpret_cast<uint32_t *>(row) = u;
+            }
+        }
+        if (lane == 0) const_cast<float *>(side ? a.c.vs : a.c.ks)[w.scale + head * a.c.sh] = bad ? NAN : zero ? 0.f : scale;
+    }
+}
+
+template <typename T, int KIND, int D, bool VEC, int RPG>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(const KvCopyArgs a) {
+    constexpr int LANES = D / 8, W = Codes<KIND>::bytes / 4;
+    const int lane = threadIdx.x & (LANES - 1), H = a.c.heads;
+    const Where w = locate<LANES, RPG>(a, lane);
+    if (!w.any) return;
+    typedef uint32_t words __attribute__((ext_vector_type(W)));
+    words u[RPG];
+    float scale[RPG];
+#pragma unroll
+    for (int j = 0; j < RPG; ++j) {
+        const int s = w.first + j, side = s >= H, head = s - side * H;
+        scale[j] = 0.f;
+        u[j] = (words)(KIND == WQ_KV_I4 ? 0x88888888u : 0u);
+        if (w.there && s < 2 * H) {
+            u[j] = *reinterpret_cast<const words *>((side ? a.c.v : a.c.k) + w.row + head * a.c.rh + (long)lane * Codes<KIND>::bytes);
+            scale[j] = (side ? a.c.vs : a.c.ks)[w.scale + head * a.c.sh];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < RPG; ++j) {
+        const int s = w.first + j, side = s >= H, head = s - side * H;
+        if (s >= 2 * H) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (KIND == WQ_KV_F16)
+                v[i] = (float)__builtin_bit_cast(f16, (uint16_t)(u[j][i / 2] >> (16 * (i & 1))));
+            else if constexpr (KIND == WQ_KV_I8)
+                v[i] = (float)(int8_t)(u[j][i / 4] >> (8 * (i & 3)));
+            else
+                v[i] = (float)((int)(u[j][0] >> (4 * i) & 15) - 8);
+            v[i] *= scale[j];
+        }
+        store8<T, VEC>((T *)(side ? a.v : a.k) + (long)w.tok * a.tok + (long)head * a.head + 8 * lane, v);
+    }
+}
+
+template <typename T, int KIND, int D, bool VEC, int RPG>
+hipError_t launch_rpg(const KvCopyArgs &a, bool write, hipStream_t st) {
+    const long groups = (long)a.b.T * ((2 * a.c.heads + RPG - 1) / RPG);
+    const dim3 grid((unsigned)((groups * (D / 8) + kThreads - 1) / kThreads)), block(kThreads);
+    if (write)
+        hipLaunchKernelGGL((kv_append_kernel<T, KIND, D, VEC, RPG>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((kv_read_kernel<T, KIND, D, VEC, RPG>), grid, block, 0, st, a);
+    return hipGetLastError();
 }
 
 template <typename T, int KIND, int D>
 hipError_t launch_d(const KvCopyArgs &a, bool write, bool vec, hipStream_t st) {
+    if (!vec) return launch_rpg<T, KIND, D, false, 1>(a, write, st);
+    // four rows a lane group once that still leaves every CU four blocks
     const long rows = (long)a.b.T * 2 * a.c.heads;
-    const long blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), block(kThreads);
-    if (write) {
-        if (vec)
-            hipLaunchKernelGGL((kv_append_kernel<T, KIND, D, true>), grid, block, 0, st, a);
-        else
-            hipLaunchKernelGGL((kv_append_kernel<T, KIND, D, false>), grid, block, 0, st, a);
-    } else {
-        if (vec)
-            hipLaunchKernelGGL((kv_read_kernel<T, KIND, D, true>), grid, block, 0, st, a);
-        else
-            hipLaunchKernelGGL((kv_read_kernel<T, KIND, D, false>), grid, block, 0, st, a);
-    }
-    return hipGetLastError();
+    if (rows * (D / 8) >= 4L * 1024 * kThreads) return launch_rpg<T, KIND, D, true, 4>(a, write, st);
+    return launch_rpg<T, KIND, D, true, 1>(a, write, st);
 }
 
 template <typename T, int KIND>

@@ -3,8 +3,8 @@
 //
 // One block takes one row and holds it in registers as fp32 from the only
 // read of x and residual to the only write of y and the sum, so the row
-// crosses HBM once in each direction; two block-wide reductions (the sum of
-// squares, and for int8 max|r*w|) share one barrier pair.
+// crosses HBM once in each direction; the block-wide reductions (the sum of
+// squares, and for int8 max|r*w|) share one barrier.
 #include "decoder.h"
 
 namespace wq {
@@ -19,63 +19,83 @@ struct IsCode<int8_t> {
     static constexpr bool value = true;
 };
 
-// VEC elements a load, NV loads a thread: n <= blockDim * NV * VEC.
+// The larger of two non-negative doubles across lanes m apart.
+__device__ __forceinline__ double max_across(double t, int m) { return fmax(t, __shfl_xor(t, m)); }
+
+// VEC elements a load, NV loads a thread: n <= blockDim * NV * VEC. w is read
+// twice (from L2) rather than held: fewer registers, more rows in flight.
 template <typename TX, typename TY, int VEC, int NV>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
     constexpr bool CODE = IsCode<TY>::value;
-    __shared__ float red[2][16];
+    __shared__ float red[16];
+    __shared__ double red64[16];
     const long row = blockIdx.x;
     const int tid = threadIdx.x, nt = blockDim.x, n = a.n;
     const TX *x = (const TX *)a.x + row * a.xs;
     const TX *res = a.res ? (const TX *)a.res + row * a.rs : nullptr;
-    float v[NV][VEC], w[NV][VEC];
+    float v[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int e = (j * nt + tid) * VEC;
-        if (e < n) {
-            load_vec<TX, VEC>(x + e, v[j]);
-            load_vec<float, VEC>(a.w + e, w[j]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j][i] = w[j][i] = 0.f;
-        }
+        for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
+        if (e < n) load_vec<TX, VEC>(x + e, v[j]);
     }
     if (res) {
+        float r[NV][VEC];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int e = (j * nt + tid) * VEC;
-            if (e < n) {
-                float r[VEC];
-                load_vec<TX, VEC>(res + e, r);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
-            }
+            for (int i = 0; i < VEC; ++i) r[j][i] = 0.f;
+            if (e < n) load_vec<TX, VEC>(res + e, r[j]);
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] += r[j][i];
     }
-    float sq = 0.f, top = 0.f;
+    float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            sq = fmaf(v[j][i], v[j][i], sq);
-            if (CODE) top = fmaxf(top, fabsf(v[j][i] * w[j][i]));
+        for (int i = 0; i < VEC; ++i) sq = fmaf(v[j][i], v[j][i], sq);
+    double top = 0.0; // max |r * w|, in fp64, where the products are exact
+    if constexpr (CODE) {
+        // rounding to fp32 keeps the order, so a thread's largest is among its products at its fp32 maximum
+        float t = 0.f, w[NV][VEC];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = (j * nt + tid) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[j][i] = 0.f;
+            if (e < n) load_vec<float, VEC>(a.w + e, w[j]);
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) t = fmaxf(t, fabsf(v[j][i] * w[j][i]));
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (fabsf(v[j][i] * w[j][i]) == t) top = fmax(top, fabs((double)v[j][i] * (double)w[j][i]));
+    }
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) {
         sq += __shfl_xor(sq, m);
-        if (CODE) top = fmaxf(top, __shfl_xor(top, m));
+        if (CODE) top = max_across(top, m);
     }
     if (nt > 64) {
         if ((tid & 63) == 0) {
-            red[0][tid >> 6] = sq;
-            if (CODE) red[1][tid >> 6] = top;
+            red[tid >> 6] = sq;
+            if (CODE) red64[tid >> 6] = top;
         }
         __syncthreads();
         sq = 0.f;
-        top = 0.f;
         for (int i = 0; i < nt >> 6; ++i) {
-            sq += red[0][i];
-            if (CODE) top = fmaxf(top, red[1][i]);
+            sq += red[i];
+            if (CODE) top = fmax(top, red64[i]);
         }
     }
     const float rstd = 1.0f / sqrtf(sq / (float)n + a.eps);
@@ -93,46 +113,32 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
         for (int j = 0; j < NV; ++j) {
             const int e = (j * nt + tid) * VEC;
             if (e < n) {
-                float o[VEC];
+                float o[VEC], w[VEC];
+                load_vec<float, VEC>(a.w + e, w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[j][i];
+                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[i];
                 store_vec<TY, VEC>(y + e, o);
             }
         }
     } else {
-        // The exact maximum of the fp64 products: the fp32 maximum is within
-        // half an ulp of it, so only products at the fp32 maximum can be it.
-        double t64 = 0.0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (fabsf(v[j][i] * w[j][i]) == top) t64 = fmax(t64, fabs((double)v[j][i] * (double)w[j][i]));
-        __shared__ double red64[16];
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) t64 = fmax(t64, __shfl_xor(t64, m));
-        if (nt > 64) {
-            if ((tid & 63) == 0) red64[tid >> 6] = t64;
-            __syncthreads();
-            for (int i = 0; i < nt >> 6; ++i) t64 = fmax(t64, red64[i]);
-        }
-        const float scale = (float)(t64 * (double)rstd / 127.0);
+        const float scale = (float)(top * (double)rstd / 127.0);
         if (tid == 0) a.y_scale[row] = scale;
         // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
-        const bool ok = top > 0.f && scale == scale;
-        const float inv = 127.0f / top;
-        const bool range = top > 1e-30f && top < 1e30f; // fp32 holds the products and inv
+        const bool ok = top > 0.0 && scale == scale;
+        const float inv = 127.0f / (float)top;
+        const bool range = top > 1e-30 && top < 1e30; // fp32 holds the products and inv
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int e = (j * nt + tid) * VEC;
             if (e < n) {
-                float o[VEC];
+                float o[VEC], w[VEC];
+                load_vec<float, VEC>(a.w + e, w);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float f = v[j][i] * w[j][i] * inv; // within 127 * 4 * 2^-24 of the quotient
+                    const float f = v[j][i] * w[i] * inv; // within 127 * 4 * 2^-24 of the quotient
                     float c = rintf(f);
                     if (!range || fabsf(f - c) > 0.4999f) // next to a border: decide in fp64
-                        c = (float)rint((double)v[j][i] * (double)w[j][i] * 127.0 / t64);
+                        c = (float)rint((double)v[j][i] * (double)w[i] * 127.0 / top);
                     o[i] = ok ? c : 0.f;
                 }
                 store_vec<TY, VEC>(y + e, o);
@@ -149,8 +155,12 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     // one row is what counts then.
     const int want = a.rows >= 2 * cus ? 256 : 1024;
     constexpr int LAST = 32768 / 1024 / VEC; // loads a thread at the longest row
+    const int sizes[] = {1, 2, 3, 4, 8, 16, 32};
     int nv = 1;
-    while (nv < LAST && (chunks + nv - 1) / nv > want) nv *= 2;
+    for (int i = 0; i < 7 && sizes[i] <= LAST; ++i) {
+        nv = sizes[i];
+        if ((chunks + nv - 1) / nv <= want) break;
+    }
     int nt = ((chunks + nv - 1) / nv + 63) / 64 * 64;
     if (nt > 1024) return hipErrorInvalidValue;
     const dim3 grid((unsigned)a.rows), block((unsigned)nt);
@@ -159,7 +169,7 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     case N:                                                                                              \
         if constexpr (N <= LAST) hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N>), grid, block, 0, st, a); \
         break;
-        WQ_NV(1) WQ_NV(2) WQ_NV(4) WQ_NV(8) WQ_NV(16) WQ_NV(32)
+        WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8) WQ_NV(16) WQ_NV(32)
 #undef WQ_NV
     default: return hipErrorInvalidValue;
     }
