@@ -84,11 +84,10 @@ struct Span {
     int base, blocks, per, splits;
 };
 
-template <int STEP>
-__device__ __forceinline__ Span find_span(int lo, int hi, int least, int nsplit) {
+__device__ __forceinline__ Span find_span(int step, int lo, int hi, int least, int nsplit) {
     Span s;
-    s.base = lo / STEP * STEP;
-    s.blocks = hi > lo ? (hi - s.base + STEP - 1) / STEP : 0;
+    s.base = lo & -step;
+    s.blocks = hi > lo ? (hi - s.base + step - 1) / step : 0;
     s.per = max(least, (s.blocks + nsplit - 1) / nsplit);
     s.splits = s.blocks == 0 ? 1 : (s.blocks + s.per - 1) / s.per;
     return s;
@@ -168,6 +167,37 @@ __device__ __forceinline__ int head_room(float top) {
     return 13 - max(e, -100);
 }
 
+// The exponent that brings a value scale of up to `big` below 2^14.
+__device__ __forceinline__ float scale_room(float big) {
+    return (float)(13 - max((int)(__float_as_uint(big) >> 23) - 127, -90));
+}
+
+// Maxima and sums across lanes 32 or 16 apart, both lanes with the same bits.
+__device__ __forceinline__ u32x2 swap32(float x) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+}
+__device__ __forceinline__ u32x2 swap16(float x) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+}
+template <int NG> // lanes that share a row: 2 (32 apart) or 4 (16 and 32 apart)
+__device__ __forceinline__ float row_max(float x) {
+    if (NG == 4) {
+        const u32x2 r = swap16(x);
+        x = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+    }
+    const u32x2 r = swap32(x);
+    return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+template <int NG>
+__device__ __forceinline__ float row_sum(float x) {
+    if (NG == 4) {
+        const u32x2 r = swap16(x);
+        x = __uint_as_float(r.x) + __uint_as_float(r.y);
+    }
+    const u32x2 r = swap32(x);
+    return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // A pair of floats as three bf16 pairs that sum to them exactly (24 bits).
@@ -187,17 +217,44 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
+// words of `bytes` (1, 2, 4, 8, 16, 32) at p
+template <int BYTES>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+    if constexpr (BYTES == 1) {
+        w[0] = *p;
+    } else if constexpr (BYTES == 2) {
+        w[0] = *reinterpret_cast<const uint16_t *>(p);
+    } else if constexpr (BYTES == 4) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (BYTES == 8) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + 16 * i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 struct AttnPlan {
-    int few_tiles;  // 16-row tiles a wave carries (few-rows kernel)
+    bool few;       // few-rows kernel, else the tiled one
+    int waves;      // waves a block (tiled kernel)
+    int rows;       // rows a tile
+    int step;       // positions a step
     int nsplit;     // most splits of a tile's positions
-    int least;      // fewest blocks of positions a split takes
-    long tiles;     // tile numbers
+    int least;      // fewest steps a split takes
     size_t ws_bytes;
 };
 
-// Partial results of a split: row (token, head) and split s at part[(row * nsplit + s) * D], their maximum
-// (base 2) and sum at ml[(row * nsplit + s) * 2].
+// Partial results of a split: row (token, head) and split s at part[(row * nsplit + s) * D], the exponent they
+// are scaled by (2^-ref) and their sum of probabilities at ml[(row * nsplit + s) * 2].
 struct Partials {
     float *part, *ml;
     int nsplit, least;

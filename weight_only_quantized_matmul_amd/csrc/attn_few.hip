@@ -39,29 +39,6 @@ struct Few {
     static constexpr int KB = TK / 16, VG = TK / 32, DT = D / 16, KS = D / 32;
 };
 
-// words of `bytes` (2, 4, 8, 16, 32) at p
-template <int BYTES>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
-    if constexpr (BYTES == 2) {
-        w[0] = *reinterpret_cast<const uint16_t *>(p);
-    } else if constexpr (BYTES == 4) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (BYTES == 8) {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i) {
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + 16 * i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
-    }
-}
-
 template <typename T, int KIND, int D, int MT, typename OFF>
 __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const Partials pt, const int vec) {
     typedef Few<T, KIND, D, MT> F;
@@ -87,7 +64,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
     int lo, hi, lo_max, hi_min;
     seen_range(t, t.row0 / G, a.causal, a.window, &lo, &hi_min);
     seen_range(t, (t.row0 + t.rows - 1) / G, a.causal, a.window, &lo_max, &hi);
-    const Span sp = find_span<TK>(lo, hi, pt.least, pt.nsplit);
+    const Span sp = find_span(TK, lo, hi, pt.least, pt.nsplit);
     if (split >= sp.splits) return;
     const int blk0 = split * sp.per, blk1 = min(sp.blocks, blk0 + sp.per);
 
@@ -122,9 +99,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                 top = fmaxf(top, fabsf(v[s][e]));
             }
         }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const int e = head_room(top);
+        const int e = head_room(row_max<4>(top));
         // the scale's sign goes to q, and a scale of zero too, so that rs > 0 and -inf * rs stays -inf
         const float up = a.scale < 0.f ? -pow2(e) : a.scale == 0.f ? 0.f : pow2(e);
         rs[mt] = fmaxf(fabsf(a.scale) * kLog2e * pow2(-e), 0x1p-126f);
@@ -203,12 +178,13 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
             }
     };
 
-    float m[MT], l[MT], c[MT];
+    float m[MT], ref[MT], e_min[MT], l[MT]; // p = 2^(s - ref), ref = m - e_min: p times any value scale stays below 2^14
     f32x4 o[MT][F::DT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        m[mt] = -INFINITY;
-        l[mt] = c[mt] = 0.f;
+        m[mt] = ref[mt] = -INFINITY;
+        e_min[mt] = F::BF ? 0.f : 127.f;
+        l[mt] = 0.f;
 #pragma unroll
         for (int d = 0; d < F::DT; ++d) o[mt][d] = f32x4{0, 0, 0, 0};
     }
@@ -308,23 +284,12 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                     top = fmaxf(top, s[mt][kb][r]);
                     if (!F::BF) big = fmaxf(big, fabsf(vsc[mt][kb][r]));
                 }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float mn = fmaxf(m[mt], top * rs[mt]);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float grow = __builtin_amdgcn_exp2f(m[mt] - base);
-            float move = grow, put = 1.f;
-            m[mt] = mn;
-            if (!F::BF) {
-                big = fmaxf(big, __shfl_xor(big, 16));
-                big = fmaxf(big, __shfl_xor(big, 32));
-                // power of two above the largest scale so far
-                const float up = __uint_as_float(__float_as_uint(big) & 0x7f800000u) * 2.f;
-                const float cn = fmaxf(c[mt], fminf(fmaxf(up, 0x1p-100f), 0x1p126f));
-                move *= c[mt] / cn;
-                put = 0x1p14f / cn;
-                c[mt] = cn;
-            }
+            m[mt] = fmaxf(m[mt], row_max<4>(top) * rs[mt]);
+            if (!F::BF) e_min[mt] = fminf(e_min[mt], scale_room(row_max<4>(big)));
+            const float was = ref[mt];
+            ref[mt] = m[mt] == -INFINITY ? -INFINITY : m[mt] - e_min[mt];
+            const float base = m[mt] == -INFINITY ? 0.f : ref[mt];
+            const float grow = __builtin_amdgcn_exp2f(was - base);
             float sum = 0.f;
 #pragma unroll
             for (int kb = 0; kb < F::KB; ++kb) {
@@ -333,7 +298,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                 for (int r = 0; r < 4; ++r) {
                     const float p = __builtin_amdgcn_exp2f(fmaf(s[mt][kb][r], rs[mt], -base));
                     sum += p;
-                    y[r] = F::BF ? p * vsc[mt][kb][r] : p * vsc[mt][kb][r] * put;
+                    y[r] = p * vsc[mt][kb][r];
                     if (KIND == WQ_KV_F16) pf[mt][kb][r] = y[r];
                 }
 #pragma unroll
@@ -351,9 +316,9 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                 }
             }
             l[mt] = l[mt] * grow + sum;
-            if (__ballot(move != 1.f)) {
+            if (__ballot(grow != 1.f)) {
 #pragma unroll
-                for (int d = 0; d < F::DT; ++d) o[mt][d] *= move;
+                for (int d = 0; d < F::DT; ++d) o[mt][d] *= grow;
             }
         }
 
@@ -494,10 +459,9 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
     // join the four waves
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        l[mt] += __shfl_xor(l[mt], 16);
-        l[mt] += __shfl_xor(l[mt], 32);
+        l[mt] = row_sum<4>(l[mt]);
         if (g == 0) {
-            sh_m[wave][mt * 16 + n] = m[mt];
+            sh_m[wave][mt * 16 + n] = ref[mt];
             sh_l[wave][mt * 16 + n] = l[mt];
         }
     }
@@ -511,7 +475,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
         L[mt] = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) L[mt] += sh_l[w][r] * __builtin_amdgcn_exp2f(sh_m[w][r] - base);
-        const float f = __builtin_amdgcn_exp2f(m[mt] - base) * (F::BF ? KIND == WQ_KV_I4 ? 16.f : 1.f : 0x1p-14f * c[mt]);
+        const float f = __builtin_amdgcn_exp2f(ref[mt] - base) * (F::BF && KIND == WQ_KV_I4 ? 16.f : 1.f);
 #pragma unroll
         for (int d = 0; d < F::DT; ++d) o[mt][d] *= f;
     }
@@ -561,7 +525,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                 pt.ml[(row * pt.nsplit + split) * 2 + 1] = L[mt];
             }
         } else {
-            const bool none = M[mt] == -INFINITY && L[mt] == 0.f;
+            const bool none = M[mt] == -INFINITY && L[mt] == 0.f; // nothing seen
             const float inv = none ? 0.f : 1.0f / L[mt];
             T *dst = (T *)a.o + (long)(t.tok0 + ti) * a.ot + (long)(kvh * G + j) * a.oh;
 #pragma unroll
@@ -584,78 +548,22 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
     }
 }
 
-// Rows whose positions were split: one wave a row joins its splits.
-template <typename T, int D, int R, int TK>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, const Partials pt) {
-    const int lane = threadIdx.x & 63;
-    const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= (long)a.b.T * a.H) return;
-    const int G = a.H / a.c.heads;
-    const int tok = (int)(row / a.H), h = (int)(row % a.H);
-    const int b = sequence_of<64>(a.b.q_start, a.b.B, tok, lane);
-    if (b >= a.b.B) return;
-    const int s0 = min(max(a.b.q_start[b], 0), a.b.T), s1 = min(max(a.b.q_start[b + 1], 0), a.b.T);
-    if (tok < s0 || tok >= s1) return;
-    // the tile that this row was in
-    Tile t;
-    const int r = (tok - s0) * G + h % G;
-    t.n = s1 - s0;
-    t.row0 = r / R * R;
-    t.rows = min(R, t.n * G - t.row0);
-    const int kv = max(a.b.kv_len[b], 0);
-    const long held = (long)a.b.width * a.c.page;
-    t.past = kv - t.n;
-    t.kv = kv < held ? kv : (int)held;
-    int lo, hi, x;
-    seen_range(t, t.row0 / G, a.causal, a.window, &lo, &x);
-    seen_range(t, (t.row0 + t.rows - 1) / G, a.causal, a.window, &x, &hi);
-    const Span sp = find_span<TK>(lo, hi, pt.least, pt.nsplit);
-    if (sp.splits <= 1) return;
-    const float *ml = pt.ml + row * pt.nsplit * 2;
-    float M = -INFINITY;
-    for (int s = lane; s < sp.splits; s += 64) M = fmaxf(M, ml[2 * s]);
-#pragma unroll
-    for (int k = 32; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor(M, k));
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, o[D / 64] = {};
-    const float *part = pt.part + row * pt.nsplit * D + lane * (D / 64);
-    for (int s = 0; s < sp.splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
-        L += ml[2 * s + 1] * f;
-        float v[D / 64];
-        load_vec<float, D / 64>(part + (long)s * D, v);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) o[k] = fmaf(v[k], f, o[k]);
-    }
-    const bool none = M == -INFINITY && L == 0.f;
-    const float inv = none ? 0.f : 1.0f / L;
-    T *dst = (T *)a.o + (long)tok * a.ot + (long)h * a.oh + lane * (D / 64);
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) dst[k] = (T)(none ? 0.f : o[k] * inv);
-    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
-}
-
 template <typename T, int KIND, int D, int MT>
 hipError_t launch_few(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
-    typedef Few<T, KIND, D, MT> F;
-    const long blocks = p.tiles * p.nsplit * a.c.heads;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    const long blocks = tile_count(a.b.T, a.H / a.c.heads, 16 * MT, a.b.B) * p.nsplit * a.c.heads;
+    if (blocks > 0x7fffffffL || p.rows != 16 * MT || p.step != Few<T, KIND, D, MT>::TK) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block(256);
     if (wide)
         hipLaunchKernelGGL((attn_few_kernel<T, KIND, D, MT, uint64_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);
     else
         hipLaunchKernelGGL((attn_few_kernel<T, KIND, D, MT, uint32_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);
-    if (p.nsplit > 1) {
-        const long rows = (long)a.b.T * a.H;
-        hipLaunchKernelGGL((attn_join_kernel<T, D, 16 * MT, F::TK>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a, pt);
-    }
     return hipGetLastError();
 }
 
 template <typename T, int KIND, int D>
 hipError_t launch_mt(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
     if constexpr (D <= 128) // two tiles of 256-element rows do not fit the registers
-        if (p.few_tiles == 2) return launch_few<T, KIND, D, 2>(a, p, pt, vec, wide, st);
+        if (p.rows == 32) return launch_few<T, KIND, D, 2>(a, p, pt, vec, wide, st);
     return launch_few<T, KIND, D, 1>(a, p, pt, vec, wide, st);
 }
 

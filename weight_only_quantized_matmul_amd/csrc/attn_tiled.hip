@@ -1,0 +1,560 @@
+// Attention of many rows a sequence and key/value head (prefill, chunks of new
+// tokens): the cache's tiles are opened once into LDS and shared by the rows.
+//
+// A block of NW waves takes a tile of RW * NW rows and walks the positions in
+// steps of TK = 64. K goes to LDS as f16 rows, V transposed, so both are read
+// back as whole 16-byte operands; the next step's codes are in flight from HBM
+// or L2 meanwhile, and two LDS buffers leave one barrier a step. Per step a
+// wave computes for its RW rows
+//     S^T[key][row]  = sum_d K[key][d] Q[row][d]           (A = K, B = Q)
+//     O^T[d][row]   += sum_key V^T[d][key] P^T[key][row]   (A = V^T, B = P^T)
+// with v_mfma_f32_32x32x16 (RW = 32) or 16x16x32 (RW = 16: rows of 256
+// elements, whose operands would not fit the registers otherwise). A lane
+// holds quads of four consecutive keys of one row in S^T; V's columns stand in
+// LDS in the order in which these quads form P^T operands, so probabilities
+// never leave their lane. Parts and scales are as in the few-rows kernel.
+#include "attn_common.h"
+
+namespace wq {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int RW>
+struct Mma;
+template <>
+struct Mma<32> {
+    typedef f32x16 acc;
+    static __device__ __forceinline__ acc f16(f16x8 a, f16x8 b, acc c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ acc bf16(f16x8 a, f16x8 b, acc c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<16> {
+    typedef f32x4 acc;
+    static __device__ __forceinline__ acc f16(f16x8 a, f16x8 b, acc c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ acc bf16(f16x8 a, f16x8 b, acc c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+
+template <typename T, int KIND, int D, int NW>
+struct Tiled {
+    static constexpr int RW = D == 256 ? 16 : 32;    // rows a wave
+    static constexpr int TK = 64, NT = 64 * NW, R = RW * NW;
+    static constexpr int NG = 64 / RW;               // lanes that share a row
+    static constexpr int CH = D / 8;                 // 16-byte chunks of a K row in LDS
+    static constexpr int KS = D / (8 * NG);          // steps of a K operand
+    static constexpr int KBN = TK / RW, DB = D / RW; // blocks of S^T and of O^T
+    static constexpr int QB = RW * RW / 256;         // quads a lane holds of a block
+    static constexpr int NQ = KBN * QB;              // quads a lane holds of a step: keys 4 NG q + 4 g + 0..3
+    static constexpr int ST = NQ / 2;                // steps of a V operand: quads 2s, 2s + 1
+    static constexpr int P = sizeof(T) == 4 ? 2 : 1; // f16 parts of q
+    static constexpr bool BF = P == 2 && KIND != WQ_KV_F16;
+    static constexpr int PP = BF ? 3 : P;            // parts of p
+    static constexpr int KU = TK * CH / NT;          // 8-code units of K a thread brings
+    static constexpr int KW = KIND == WQ_KV_F16 ? 4 : KIND == WQ_KV_I8 ? 2 : 1; // words of one
+    static constexpr int VK = TK * 32 / NT;          // keys of V a thread brings, D / 32 codes each
+    static constexpr int VE = D / 32;
+    static constexpr int VB = KIND == WQ_KV_F16 ? 2 * VE : KIND == WQ_KV_I8 ? VE : VE / 2;
+    static constexpr int VW = VB < 4 ? 1 : VB / 4;
+};
+
+// where chunk c of row r stands in LDS, in 16-byte chunks
+template <int CH>
+__device__ __forceinline__ int k_at(int r, int c) { return r * CH + (c ^ (r & (CH < 16 ? 7 : 15))); }
+__device__ __forceinline__ int v_at(int d, int c) { return d * 8 + (c ^ ((d ^ (d >> 2)) & 7)); }
+
+template <typename T, int KIND, int D, int NW, typename OFF>
+__global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, const Partials pt, const int vec) {
+    typedef Tiled<T, KIND, D, NW> F;
+    constexpr int RW = F::RW, NG = F::NG, TK = F::TK, P = F::P;
+    typedef typename Mma<RW>::acc acc;
+    __shared__ u32x4 sk[2][TK * F::CH];
+    __shared__ u32x4 sv[2][D * 8];
+    __shared__ OFF s_off[2][TK];
+    __shared__ float s_ks[2][TK], s_vs[2][TK], s_big[2];
+    __shared__ uint64_t s_mask[2];
+    __shared__ int s_bad[3]; // of step i at i % 3: set a step before its use, cleared a step after
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & (RW - 1), g = lane / RW;
+    const int G = a.H / a.c.heads;
+    const int kvh = blockIdx.x % a.c.heads;
+    const long rest = blockIdx.x / a.c.heads;
+    const int split = (int)(rest % pt.nsplit);
+    // later tiles see more positions (causal): they start first
+    const long ids = tile_count(a.b.T, G, F::R, a.b.B);
+    const Tile t = find_tile<F::R>(a.b, a.c.page, G, ids - 1 - rest / pt.nsplit, lane);
+    if (t.rows == 0) return;
+    int lo, hi, lo_max, hi_min;
+    seen_range(t, t.row0 / G, a.causal, a.window, &lo, &hi_min);
+    seen_range(t, (t.row0 + t.rows - 1) / G, a.causal, a.window, &lo_max, &hi);
+    const Span sp = find_span(TK, lo, hi, pt.least, pt.nsplit);
+    if (split >= sp.splits) return;
+    const int blk0 = split * sp.per, blk1 = min(sp.blocks, blk0 + sp.per);
+
+    // this lane's row and Q
+    const int r_in = wave * RW + n;
+    const bool live = r_in < t.rows;
+    const int row = t.row0 + (live ? r_in : 0), tok = row / G, head = kvh * G + row % G;
+    int row_lo, row_hi;
+    seen_range(t, tok, a.causal, a.window, &row_lo, &row_hi);
+    // what the wave's rows see: nothing outside [w_lo, w_hi), all of [w_lo_max, w_hi_min)
+    int w_lo = 0, w_hi = 0, w_lo_max = 0, w_hi_min = 0;
+    const bool working = wave * RW < t.rows;
+    if (working) {
+        seen_range(t, (t.row0 + wave * RW) / G, a.causal, a.window, &w_lo, &w_hi_min);
+        seen_range(t, (t.row0 + min(wave * RW + RW, t.rows) - 1) / G, a.causal, a.window, &w_lo_max, &w_hi);
+    }
+    float rs;
+    f16x8 q[F::KS][P];
+    {
+        const T *src = (const T *)a.q + (long)(t.tok0 + tok) * a.qt + (long)head * a.qh;
+        float top = 0.f;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            float up = 1.f;
+            if (pass == 1) {
+                const int e = head_room(row_max<NG>(top));
+                // the scale's sign goes to q, and a scale of zero too, so that rs > 0 and -inf * rs stays -inf
+                up = a.scale < 0.f ? -pow2(e) : a.scale == 0.f ? 0.f : pow2(e);
+                rs = fmaxf(fabsf(a.scale) * kLog2e * pow2(-e), 0x1p-126f);
+            }
+#pragma unroll
+            for (int s = 0; s < F::KS; ++s) {
+                const int d0 = (s * NG + g) * 8;
+                float u[8], v[8];
+                if (vec) {
+                    load_vec<T, 8>(src + d0, u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = (float)src[d0 + e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = live ? u[k_order<KIND>(e)] : 0.f;
+                if (pass == 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                } else {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x0 = v[2 * k] * up, x1 = v[2 * k + 1] * up;
+                        h[k] = pack_half(x0, x1);
+                        if (P == 2) {
+                            const f16x2 y = __builtin_bit_cast(f16x2, h[k]);
+                            l[k] = pack_half(x0 - (float)y.x, x1 - (float)y.y);
+                        }
+                    }
+                    q[s][0] = join4(h);
+                    if (P == 2) q[s][P - 1] = join4(l);
+                }
+            }
+        }
+    }
+
+    const OpenConst oc;
+    const uint8_t *kp = a.c.k + (long)kvh * a.c.rh, *vp = a.c.v + (long)kvh * a.c.rh;
+    const float *ksp = a.c.ks + (long)kvh * a.c.sh, *vsp = a.c.vs + (long)kvh * a.c.sh;
+    const int *table = a.b.table + (long)t.b * a.b.table_stride;
+
+    // Page and place of position `lane` of step i (wave 0); positions that are not there take row 0, which exists.
+    struct Key {
+        int page, slot;
+        bool there;
+    };
+    auto look = [&](int i) {
+        Key k;
+        const int pos = sp.base + i * TK + lane;
+        k.there = i < blk1 && pos >= lo && pos < hi;
+        const int idx = page_index(a.c, pos);
+        k.slot = pos - idx * a.c.page;
+        k.page = k.there ? table[idx] : -1;
+        return k;
+    };
+    struct Place {
+        OFF row, scale;
+        bool ok;
+        uint64_t mask;
+    };
+    auto place = [&](const Key &k) {
+        Place p;
+        p.ok = k.there && k.page >= 0 && k.page < a.c.pages;
+        const OFF page = p.ok ? k.page : 0, slot = p.ok ? k.slot : 0;
+        p.row = page * (OFF)a.c.rp + slot * (OFF)a.c.rs;
+        p.scale = page * (OFF)a.c.sp + slot * (OFF)a.c.ss;
+        p.mask = __ballot(p.ok);
+        return p;
+    };
+    auto put_scales = [&](int buf, bool ok, float ks, float vs) {
+        vs = ok ? vs : 0.f;
+        s_ks[buf][lane] = ok ? ks : 0.f;
+        s_vs[buf][lane] = vs;
+        if (!F::BF) {
+            float big = fabsf(vs);
+#pragma unroll
+            for (int m = 32; m > 0; m >>= 1) big = fmaxf(big, __shfl_xor(big, m));
+            if (lane == 0) s_big[buf] = big;
+        }
+    };
+
+    // A thread's share of a step: KU units of K, VK keys of V.
+    uint32_t rk[F::KU][F::KW], rv[F::VK][F::VW];
+    const int dg = tid & 31, hc = tid >> 5;
+    const int vc = F::VK == 8 ? hc : hc >> 1; // its chunk of V^T: keys v0 .. v0+3 and (VK = 8) v0 + 4 NG .. + 3
+    const int v0 = (vc / NG) * 8 * NG + (vc % NG) * 4 + (F::VK == 8 ? 0 : (hc & 1) * 4 * NG);
+    auto fetch = [&](int buf) {
+#pragma unroll
+        for (int u = 0; u < F::KU; ++u) {
+            const int x = u * F::NT + tid;
+            load_words<4 * F::KW>(kp + (s_off[buf][x / F::CH] + (OFF)((x % F::CH) * 4 * F::KW)), rk[u]);
+        }
+#pragma unroll
+        for (int k = 0; k < F::VK; ++k)
+            load_words<F::VB>(vp + (s_off[buf][v0 + (k & 3) + (k >> 2) * 4 * NG] + (OFF)(dg * F::VB)), rv[k]);
+    };
+    // ... opened into LDS. `edge`: some rows see less than others or not every position is there.
+    auto store = [&](int buf, int step, uint64_t mask, bool edge) {
+#pragma unroll
+        for (int u = 0; u < F::KU; ++u) {
+            const int x = u * F::NT + tid;
+            uint32_t w[4];
+            if constexpr (KIND == WQ_KV_F16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = rk[u][k];
+            } else if constexpr (KIND == WQ_KV_I8) {
+                open_i8(rk[u][0], w);
+                open_i8(rk[u][1], w + 2);
+            } else {
+                open_i4(oc, rk[u][0], w);
+            }
+            sk[buf][k_at<F::CH>(x / F::CH, x % F::CH)] = u32x4{w[0], w[1], w[2], w[3]};
+        }
+        if constexpr (KIND == WQ_KV_F16) {
+            // An infinity or a NaN among the codes must not reach rows that do not see it (0 * NaN):
+            // where rows differ in what they see, such codes leave the operands and are taken one by one.
+            if (edge) {
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < F::VK; ++k) {
+                    const bool gone = !(mask >> (v0 + (k & 3) + (k >> 2) * 4 * NG) & 1);
+#pragma unroll
+                    for (int w = 0; w < F::VW; ++w) {
+                        uint32_t x = gone ? 0u : rv[k][w];
+                        const bool b0 = (x & 0x7c00u) == 0x7c00u, b1 = (x & 0x7c000000u) == 0x7c000000u;
+                        bad = bad || b0 || b1;
+                        x = b0 ? x & 0xffff0000u : x;
+                        rv[k][w] = b1 ? x & 0xffffu : x;
+                    }
+                }
+                if (bad) s_bad[step % 3] = 1;
+            }
+        }
+        uint32_t o[F::VE][F::VK / 2];
+#pragma unroll
+        for (int k = 0; k < F::VK / 2; ++k) {
+            const uint32_t *x = rv[2 * k], *y = rv[2 * k + 1];
+            if constexpr (KIND == WQ_KV_F16) {
+#pragma unroll
+                for (int e = 0; e < F::VE; ++e) o[e][k] = __builtin_amdgcn_perm(y[e / 2], x[e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+            } else if constexpr (KIND == WQ_KV_I8) {
+#pragma unroll
+                for (int e = 0; e < F::VE; ++e) {
+                    const uint32_t sel = 0x0c000c00u | (uint32_t)(e & 3) | (uint32_t)(4 + (e & 3)) << 16;
+                    o[e][k] = F::BF ? high_halves(byte_i8(x[e / 4], e & 3), byte_i8(y[e / 4], e & 3))
+                                    : pk_add(__builtin_amdgcn_perm(y[e / 4], x[e / 4], sel) ^ 0x64806480u, -1152.f);
+                }
+            } else if constexpr (F::BF) {
+                const uint32_t x0 = x[0] ^ 0x88888888u, y0 = y[0] ^ 0x88888888u, x1 = x0 >> 4, y1 = y0 >> 4;
+#pragma unroll
+                for (int e = 0; e < F::VE; ++e)
+                    o[e][k] = e & 1 ? high_halves(nibble_i4(x1, e / 2), nibble_i4(y1, e / 2)) : high_halves(nibble_i4(x0, e / 2), nibble_i4(y0, e / 2));
+            } else {
+#pragma unroll
+                for (int e = 0; e < F::VE; e += 4) {
+                    uint32_t w[4];
+                    open_i4(oc, __builtin_amdgcn_perm(y[0], x[0], e ? 0x07060302u : 0x05040100u), w);
+#pragma unroll
+                    for (int j = 0; j < 4 && e + j < F::VE; ++j) o[e + j][k] = w[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < F::VE; ++e) {
+            const int d = dg * F::VE + e;
+            if constexpr (F::VK == 8)
+                sv[buf][v_at(d, vc)] = u32x4{o[e][0], o[e][1], o[e][2], o[e][3]};
+            else
+                reinterpret_cast<u32x2 *>(&sv[buf][v_at(d, vc)])[hc & 1] = u32x2{o[e][0], o[e][1]};
+        }
+    };
+    constexpr uint64_t all = ~0ull;
+    auto is_edge = [&](int i, uint64_t mask) {
+        const int t0 = sp.base + i * TK;
+        return mask != all || t0 < lo_max || t0 + TK > hi_min;
+    };
+
+    float ref = -INFINITY, m = -INFINITY, l = 0.f; // p = 2^(s - ref)
+    float e_min = F::BF ? 0.f : 127.f;             // ref = m - e_min: 2^e_min brings the values' scales below 2^14
+    acc o[F::DB];
+#pragma unroll
+    for (int d = 0; d < F::DB; ++d)
+#pragma unroll
+        for (int k = 0; k < 4 * F::QB; ++k) o[d][k] = 0.f;
+
+    // fill: offsets of steps blk0 and blk0 + 1, codes and scales of blk0
+    Place next;
+    if (wave == 0) {
+        const Place p0 = place(look(blk0));
+        next = place(look(blk0 + 1));
+        s_off[0][lane] = p0.row;
+        s_off[1][lane] = next.row;
+        put_scales(0, p0.ok, ksp[p0.scale], vsp[p0.scale]);
+        if (lane == 0) {
+            s_mask[0] = p0.mask;
+            s_mask[1] = next.mask;
+            s_bad[0] = s_bad[1] = s_bad[2] = 0;
+        }
+    }
+    __syncthreads();
+    if (blk1 > blk0) {
+        fetch(0);
+        store(0, 0, s_mask[0], is_edge(blk0, s_mask[0]));
+    }
+    __syncthreads();
+
+    for (int i = blk0, buf = 0; i < blk1; ++i, buf ^= 1) {
+        const int t0 = sp.base + i * TK;
+        const uint64_t mask = s_mask[buf], mask_next = s_mask[buf ^ 1];
+        fetch(buf ^ 1); // past the last step: row 0 again, unused
+        Key after;
+        float ks1 = 0.f, vs1 = 0.f;
+        if (wave == 0) {
+            after = look(i + 2);
+            ks1 = ksp[next.scale];
+            vs1 = vsp[next.scale];
+        }
+        if (working && t0 < w_hi && t0 + TK > w_lo) {
+            acc s[F::KBN];
+#pragma unroll
+            for (int kb = 0; kb < F::KBN; ++kb) {
+#pragma unroll
+                for (int k = 0; k < 4 * F::QB; ++k) s[kb][k] = 0.f;
+#pragma unroll
+                for (int st = 0; st < F::KS; ++st) {
+                    const f16x8 kf = __builtin_bit_cast(f16x8, sk[buf][k_at<F::CH>(kb * RW + n, st * NG + g)]);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) s[kb] = Mma<RW>::f16(kf, q[st][k], s[kb]);
+                }
+            }
+            float vsc[F::NQ][4];
+#pragma unroll
+            for (int j = 0; j < F::NQ; ++j) {
+                const f32x4 ks = *reinterpret_cast<const f32x4 *>(&s_ks[buf][4 * NG * j + 4 * g]);
+                const f32x4 vs = *reinterpret_cast<const f32x4 *>(&s_vs[buf][4 * NG * j + 4 * g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j / F::QB][4 * (j % F::QB) + e] *= ks[e];
+                    vsc[j][e] = vs[e];
+                }
+            }
+            float big = s_big[buf];
+            const bool edge = mask != all || t0 < w_lo_max || t0 + TK > w_hi_min;
+            if (edge) { // a key that a row does not see scores -inf there and has scale 0, whatever it held
+                const uint64_t own = mask >> (4 * g);
+                const int from = row_lo - t0 - 4 * g, to = row_hi - t0 - 4 * g;
+                big = 0.f;
+#pragma unroll
+                for (int j = 0; j < F::NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int k = 4 * NG * j + e;
+                        const bool on = (own >> k & 1) && k >= from && k < to;
+                        s[j / F::QB][4 * (j % F::QB) + e] = on ? s[j / F::QB][4 * (j % F::QB) + e] : -INFINITY;
+                        vsc[j][e] = on ? vsc[j][e] : 0.f;
+                        big = fmaxf(big, fabsf(vsc[j][e]));
+                    }
+                if (!F::BF) big = row_max<NG>(big);
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < F::NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j / F::QB][4 * (j % F::QB) + e]);
+            m = fmaxf(m, row_max<NG>(top) * rs);
+            if (!F::BF) e_min = fminf(e_min, scale_room(big));
+            const float was = ref;
+            ref = m == -INFINITY ? -INFINITY : m - e_min;
+            const float base = m == -INFINITY ? 0.f : ref;
+            const float grow = __builtin_amdgcn_exp2f(was - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < F::NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(fmaf(s[j / F::QB][4 * (j % F::QB) + e], rs, -base));
+                    sum += p;
+                    s[j / F::QB][4 * (j % F::QB) + e] = p * vsc[j][e];
+                }
+            l = l * grow + sum;
+            if (__ballot(grow != 1.f)) {
+#pragma unroll
+                for (int d = 0; d < F::DB; ++d) o[d] *= grow;
+            }
+            if constexpr (KIND == WQ_KV_F16) {
+                if (s_bad[(i - blk0) % 3]) {
+                    for (int key = 0; key < TK; ++key) {
+                        if (!(mask >> key & 1)) continue;
+                        // the row's offset is no longer in LDS: look it up again
+                        const int pos = t0 + key, idx = page_index(a.c, pos);
+                        const f16 *src = (const f16 *)(vp + ((OFF)table[idx] * (OFF)a.c.rp + (OFF)(pos - idx * a.c.page) * (OFF)a.c.rs));
+                        float y = 0.f;
+#pragma unroll
+                        for (int j = 0; j < F::NQ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (j == key / (4 * NG) && e == (key & 3)) y = s[j / F::QB][4 * (j % F::QB) + e];
+                        y = __shfl(y, (key >> 2 & (NG - 1)) * RW + n);
+                        if (pos >= row_lo && pos < row_hi) {
+#pragma unroll
+                            for (int d = 0; d < F::DB; ++d)
+#pragma unroll
+                                for (int k = 0; k < 4 * F::QB; ++k) {
+                                    const float code = (float)src[d * RW + 4 * NG * (k >> 2) + 4 * g + (k & 3)];
+                                    if (!(fabsf(code) < INFINITY)) o[d][k] = fmaf(y, code, o[d][k]);
+                                }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < F::ST; ++st) {
+                uint32_t pb[F::PP][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = 2 * st + (k >> 1), at = 4 * (j % F::QB) + 2 * (k & 1);
+                    const float y0 = s[j / F::QB][at], y1 = s[j / F::QB][at + 1];
+                    if constexpr (F::BF) {
+                        uint32_t w[3];
+                        split3(y0, y1, w);
+                        pb[0][k] = w[0];
+                        pb[1][k] = w[1];
+                        pb[2][k] = w[2];
+                    } else {
+                        pb[0][k] = pack_half(y0, y1);
+                        if constexpr (F::PP == 2) {
+                            const f16x2 z = __builtin_bit_cast(f16x2, pb[0][k]);
+                            pb[1][k] = pack_half(y0 - (float)z.x, y1 - (float)z.y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < F::DB; ++d) {
+                    const f16x8 vf = __builtin_bit_cast(f16x8, sv[buf][v_at(d * RW + n, st * NG + g)]);
+#pragma unroll
+                    for (int k = 0; k < F::PP; ++k) o[d] = F::BF ? Mma<RW>::bf16(vf, join4(pb[k]), o[d]) : Mma<RW>::f16(vf, join4(pb[k]), o[d]);
+                }
+            }
+        }
+        if (KIND == WQ_KV_F16 && tid == 0) s_bad[(i - blk0 + 2) % 3] = 0;
+        store(buf ^ 1, i + 1 - blk0, mask_next, is_edge(i + 1, mask_next));
+        if (wave == 0) {
+            const Place p2 = place(after);
+            put_scales(buf ^ 1, next.ok, ks1, vs1);
+            s_off[buf][lane] = p2.row;
+            if (lane == 0) s_mask[buf] = p2.mask;
+            next = p2;
+        }
+        __syncthreads();
+    }
+
+    if (!working) return;
+    l = row_sum<NG>(l);
+    if (!live) return;
+    const long at = (long)(t.tok0 + tok) * a.H + head;
+    constexpr float unit = F::BF && KIND == WQ_KV_I4 ? 16.f : 1.f;
+    if (sp.splits > 1) {
+        float *dst = pt.part + (at * pt.nsplit + split) * D;
+#pragma unroll
+        for (int d = 0; d < F::DB; ++d)
+#pragma unroll
+            for (int j = 0; j < F::QB; ++j)
+                *reinterpret_cast<f32x4 *>(dst + d * RW + 4 * NG * j + 4 * g) =
+                    f32x4{o[d][4 * j] * unit, o[d][4 * j + 1] * unit, o[d][4 * j + 2] * unit, o[d][4 * j + 3] * unit};
+        if (g == 0) {
+            pt.ml[(at * pt.nsplit + split) * 2] = ref;
+            pt.ml[(at * pt.nsplit + split) * 2 + 1] = l;
+        }
+        return;
+    }
+    const bool none = m == -INFINITY && l == 0.f;
+    const float inv = none ? 0.f : unit / l;
+    T *dst = (T *)a.o + (long)(t.tok0 + tok) * a.ot + (long)head * a.oh;
+#pragma unroll
+    for (int d = 0; d < F::DB; ++d)
+#pragma unroll
+        for (int j = 0; j < F::QB; ++j) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = none ? 0.f : o[d][4 * j + e] * inv;
+            T *p = dst + d * RW + 4 * NG * j + 4 * g;
+            if (vec) {
+                store_vec<T, 4>(p, y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = (T)y[e];
+            }
+        }
+    if (a.lse && g == 0) a.lse[at] = none ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <typename T, int KIND, int D, int NW>
+hipError_t launch_nw(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
+    typedef Tiled<T, KIND, D, NW> F;
+    const long blocks = tile_count(a.b.T, a.H / a.c.heads, F::R, a.b.B) * p.nsplit * a.c.heads;
+    if (blocks > 0x7fffffffL || p.rows != F::R) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), block(F::NT);
+    if (wide)
+        hipLaunchKernelGGL((attn_tiled_kernel<T, KIND, D, NW, uint64_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);
+    else
+        hipLaunchKernelGGL((attn_tiled_kernel<T, KIND, D, NW, uint32_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);
+    return hipGetLastError();
+}
+
+template <typename T, int KIND, int D>
+hipError_t launch_d(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
+    return p.waves == 8 ? launch_nw<T, KIND, D, 8>(a, p, pt, vec, wide, st) : launch_nw<T, KIND, D, 4>(a, p, pt, vec, wide, st);
+}
+
+template <typename T, int KIND>
+hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int dim, bool vec, bool wide, hipStream_t st) {
+    switch (dim) {
+    case 64: return launch_d<T, KIND, 64>(a, p, pt, vec, wide, st);
+    case 128: return launch_d<T, KIND, 128>(a, p, pt, vec, wide, st);
+    default: return launch_d<T, KIND, 256>(a, p, pt, vec, wide, st);
+    }
+}
+
+template <typename T>
+hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int kind, int dim, bool vec, bool wide, hipStream_t st) {
+    switch (kind) {
+    case WQ_KV_F16: return launch_dim<T, WQ_KV_F16>(a, p, pt, dim, vec, wide, st);
+    case WQ_KV_I8: return launch_dim<T, WQ_KV_I8>(a, p, pt, dim, vec, wide, st);
+    default: return launch_dim<T, WQ_KV_I4>(a, p, pt, dim, vec, wide, st);
+    }
+}
+
+} // namespace
+
+hipError_t launch_attn_tiled(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int kind, int dim, int dtype, bool vec,
+                             bool wide, hipStream_t st) {
+    switch (dtype) {
+    case WQ_DT_F32: return launch_t<float>(a, p, pt, kind, dim, vec, wide, st);
+    case WQ_DT_BF16: return launch_t<bf16>(a, p, pt, kind, dim, vec, wide, st);
+    default: return launch_t<f16>(a, p, pt, kind, dim, vec, wide, st);
+    }
+}
+
+} // namespace wq

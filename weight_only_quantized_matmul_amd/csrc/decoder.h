@@ -91,6 +91,10 @@ struct Partials;
 hipError_t launch_attn_few(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int kind, int dim, int dtype, bool vec,
                            bool wide, hipStream_t st);
 
+hipError_t launch_attn_tiled(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int kind, int dim, int dtype, bool vec,
+                             bool wide, hipStream_t st);
+hipError_t launch_attn_join(const AttnArgs &a, const AttnPlan &p, const Partials &pt, int dim, int dtype, hipStream_t st);
+
 } // namespace wq
 
 // ---------------------------------------------------------------------------

@@ -124,18 +124,31 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     if (b->max_kv > 0 && b->max_kv < kv) kv = b->max_kv;
     if (window > 0 && causal && (long)window + q < kv) kv = (long)window + q;
     const int row = c->kind == WQ_KV_F16 ? 2 * c->dim : c->kind == WQ_KV_I8 ? c->dim : c->dim / 2;
-    const int step = row <= 128 ? 64 : 32;
-    p.few_tiles = q * G > 16 && c->dim <= 128 ? 2 : 1;
-    const long R = 16 * p.few_tiles;
-    p.tiles = wq::tile_count(b->T, G, R, b->B);
-    // tiles that are there: the numbers left unused by whole sequences not counted
-    const long full = (q * G + R - 1) / R * b->B;
-    const long blocks = (kv + step - 1) / step + 1;
-    const long total = (full < p.tiles ? full : p.tiles) * c->heads * blocks;
-    long per_wave = total / (cus * 12);
-    per_wave = per_wave < 1 ? 1 : per_wave > 8 ? 8 : per_wave;
-    p.least = (int)(4 * per_wave);
-    long n = (blocks + p.least - 1) / p.least;
+    p.few = q * G <= (c->dim <= 128 ? 32 : 16);
+    p.waves = 4;
+    if (p.few) {
+        p.rows = q * G > 16 ? 32 : 16;
+        p.step = row <= 128 ? 64 : 32;
+    } else {
+        // eight waves share each opened tile when their larger tiles still give every CU a block
+        const long wave_rows = c->dim == 256 ? 16 : 32;
+        if ((q * G + 8 * wave_rows - 1) / (8 * wave_rows) * b->B * c->heads >= cus) p.waves = 8;
+        p.rows = (int)wave_rows * p.waves;
+        p.step = 64;
+    }
+    // tiles that are there (the numbers that whole sequences leave unused not counted), and their steps
+    const long tiles = (q * G + p.rows - 1) / p.rows * b->B, numbers = wq::tile_count(b->T, G, p.rows, b->B);
+    const long steps = (kv + p.step - 1) / p.step + 1;
+    const long total = (tiles < numbers ? tiles : numbers) * c->heads * steps;
+    if (p.few) {
+        long per_wave = total / (cus * 12);
+        per_wave = per_wave < 1 ? 1 : per_wave > 8 ? 8 : per_wave;
+        p.least = (int)(4 * per_wave);
+    } else {
+        const long per_block = total / (2 * cus);
+        p.least = (int)(per_block < 4 ? 4 : per_block > steps ? steps : per_block);
+    }
+    long n = (steps + p.least - 1) / p.least;
     const long rows = (long)b->T * H;
     const long cap = (256L << 20) / (rows * (c->dim + 2) * 4); // workspace of at most 256 MiB
     n = n > 512 ? 512 : n;
@@ -316,7 +329,10 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
     };
     const bool wide = extent(cache->row_stride) + 2 * cache->dim >= 4294967296.0 ||
                       4 * (extent(cache->scale_stride) + 1) >= 4294967296.0;
-    return status(wq::launch_attn_few(a, p, pt, cache->kind, cache->dim, dtype, vec, wide, (hipStream_t)hip_stream));
+    hipError_t e = p.few ? wq::launch_attn_few(a, p, pt, cache->kind, cache->dim, dtype, vec, wide, (hipStream_t)hip_stream)
+                         : wq::launch_attn_tiled(a, p, pt, cache->kind, cache->dim, dtype, vec, wide, (hipStream_t)hip_stream);
+    if (e == hipSuccess && p.nsplit > 1) e = wq::launch_attn_join(a, p, pt, cache->dim, dtype, (hipStream_t)hip_stream);
+    return status(e);
 }
 
 } // extern "C"
