@@ -34,37 +34,37 @@ __host__ __device__ inline long tile_count(long T, long G, long R, long B) { ret
 
 template <int R>
 __device__ __forceinline__ Tile find_tile(const BatchView &b, int page, int G, long id, int lane) {
-    int hit = -1;
-    for (int i0 = 0; i0 < b.B; i0 += 64) {
-        const int i = i0 + lane;
-        bool mine = false;
-        if (i < b.B) {
-            const long s0 = min(max(b.q_start[i], 0), b.T), s1 = min(max(b.q_start[i + 1], 0), b.T);
-            const long first = s0 * G / R + i, last = s1 * G / R + i;
-            mine = s1 > s0 && id >= first && id <= last;
-        }
-        const uint64_t m = __ballot(mine);
-        if (m) {
-            hit = i0 + __builtin_ctzll(m);
-            break;
-        }
-    }
     Tile t;
     t.rows = 0;
     t.b = t.tok0 = t.n = t.row0 = t.kv = t.past = 0;
-    if (hit < 0) return t;
-    hit = __builtin_amdgcn_readfirstlane(hit);
-    const int s0 = min(max(b.q_start[hit], 0), b.T), s1 = min(max(b.q_start[hit + 1], 0), b.T);
-    const long row0 = (id - ((long)s0 * G / R + hit)) * R, all = (long)(s1 - s0) * G;
-    t.b = hit;
-    t.tok0 = s0;
-    t.n = s1 - s0;
-    t.row0 = (int)row0;
-    t.rows = row0 < all ? (int)min((long)R, all - row0) : 0;
-    const int kv = max(b.kv_len[hit], 0);
-    const long held = (long)b.width * page;
-    t.past = kv - t.n;
-    t.kv = kv < held ? kv : (int)held;
+    for (int i0 = 0; i0 < b.B; i0 += 64) {
+        const int i = i0 + lane;
+        bool mine = false;
+        int s0 = 0, s1 = 0, kv = 0;
+        if (i < b.B) {
+            s0 = b.q_start[i];
+            s1 = b.q_start[i + 1];
+            kv = b.kv_len[i]; // with the others, not after them: the chain of loads is what a short call waits for
+            s0 = min(max(s0, 0), b.T);
+            s1 = min(max(s1, 0), b.T);
+            mine = s1 > s0 && id >= (long)s0 * G / R + i && id <= (long)s1 * G / R + i;
+        }
+        const uint64_t m = __ballot(mine);
+        if (!m) continue;
+        const int hit = __builtin_ctzll(m);
+        t.b = i0 + hit;
+        t.tok0 = __builtin_amdgcn_readlane(s0, hit);
+        t.n = __builtin_amdgcn_readlane(s1, hit) - t.tok0;
+        kv = max(__builtin_amdgcn_readlane(kv, hit), 0);
+        // a sequence's last tile comes first: under a causal mask it sees the most
+        const long all = (long)t.n * G, row0 = ((all + R - 1) / R - 1 - (id - ((long)t.tok0 * G / R + t.b))) * R;
+        t.row0 = (int)max(row0, 0L);
+        t.rows = row0 >= 0 ? (int)min((long)R, all - row0) : 0;
+        const long held = (long)b.width * page;
+        t.past = kv - t.n;
+        t.kv = kv < held ? kv : (int)held;
+        return t;
+    }
     return t;
 }
 
@@ -78,8 +78,22 @@ __device__ __forceinline__ void seen_range(const Tile &t, int i, int causal, int
     *lo = (int)(l > *hi ? *hi : l);
 }
 
-// Blocks of STEP positions that the rows of a tile see, and their split:
-// `per` blocks a split, so the split does not depend on what the host knows.
+// Bits `from` .. `to` - 1 of `keys` (a lane's keys of a step that are there), the others cleared.
+__device__ __forceinline__ uint64_t seen_bits(uint64_t keys, int from, int to) {
+    from = min(max(from, 0), 64);
+    to = min(max(to, 0), 64);
+    const uint64_t below = to == 64 ? ~0ull : (1ull << to) - 1, first = from == 64 ? ~0ull : (1ull << from) - 1;
+    return keys & below & ~first;
+}
+
+// x where bit k is set, else `other`: a bit extract and a bitwise select, no branch.
+__device__ __forceinline__ float where_seen(uint64_t bits, int k, float x, float other) {
+    const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)(uint32_t)(k < 32 ? bits : bits >> 32), k & 31, 1);
+    return __uint_as_float((m & __float_as_uint(x)) | (~m & __float_as_uint(other)));
+}
+
+// Blocks of `step` positions that the rows of a tile see, and their split: `per`
+// blocks each, at least `least` where there are as many and at most nsplit splits.
 struct Span {
     int base, blocks, per, splits;
 };
@@ -88,8 +102,10 @@ __device__ __forceinline__ Span find_span(int step, int lo, int hi, int least, i
     Span s;
     s.base = lo & -step;
     s.blocks = hi > lo ? (hi - s.base + step - 1) / step : 0;
-    s.per = max(least, (s.blocks + nsplit - 1) / nsplit);
-    s.splits = s.blocks == 0 ? 1 : (s.blocks + s.per - 1) / s.per;
+    const int most = max(least, (s.blocks + nsplit - 1) / nsplit);
+    s.splits = max(1, (s.blocks + most - 1) / most);
+    s.per = (s.blocks + s.splits - 1) / s.splits; // splits of equal length
+    s.splits = max(1, s.per == 0 ? 1 : (s.blocks + s.per - 1) / s.per);
     return s;
 }
 
@@ -167,9 +183,9 @@ __device__ __forceinline__ int head_room(float top) {
     return 13 - max(e, -100);
 }
 
-// The exponent that brings a value scale of up to `big` below 2^14.
-__device__ __forceinline__ float scale_room(float big) {
-    return (float)(13 - max((int)(__float_as_uint(big) >> 23) - 127, -90));
+// The exponent that brings a value scale of up to `big` below 2^room.
+__device__ __forceinline__ float scale_room(float big, int room) {
+    return (float)(room - 1 - max((int)(__float_as_uint(big) >> 23) - 127, -90));
 }
 
 // Maxima and sums across lanes 32 or 16 apart, both lanes with the same bits.
@@ -196,6 +212,18 @@ __device__ __forceinline__ float row_sum(float x) {
     }
     const u32x2 r = swap32(x);
     return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// The maximum over the wave, in every lane (x >= 0).
+__device__ __forceinline__ float wave_max(float x) {
+    x = row_max<4>(x);
+#define WQ_ROR(n) x = fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x120 + n, 0xf, 0xf, true)))
+    WQ_ROR(8); // row_ror: lanes of a row of 16, rotated
+    WQ_ROR(4);
+    WQ_ROR(2);
+    WQ_ROR(1);
+#undef WQ_ROR
+    return x;
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -243,6 +271,9 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
 }
 
 // ---------------------------------------------------------------------------
+// Rows a wave of the tiled kernel takes: 16 where 32 rows' operands and sums do not fit its registers.
+constexpr int tiled_rows(int dim, bool f32) { return dim == 256 || (dim == 128 && f32) ? 16 : 32; }
+
 struct AttnPlan {
     bool few;       // few-rows kernel, else the tiled one
     int waves;      // waves a block (tiled kernel)

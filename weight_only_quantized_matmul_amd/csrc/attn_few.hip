@@ -68,57 +68,66 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
     if (split >= sp.splits) return;
     const int blk0 = split * sp.per, blk1 = min(sp.blocks, blk0 + sp.per);
 
-    // rows of this lane, and Q
+    // rows of this lane; Q as it comes
     int row_lo[MT], row_hi[MT];
-    float rs[MT];
-    f16x8 q[MT][F::KS][P];
+    bool live[MT];
+    float qv[MT][F::KS][8];
+    auto load_q = [&]() {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 16 + n;
-        const bool live = r < t.rows;
-        const int i = (t.row0 + (live ? r : 0)) / G, j = (t.row0 + (live ? r : 0)) % G;
-        seen_range(t, i, a.causal, a.window, &row_lo[mt], &row_hi[mt]);
-        const T *src = (const T *)a.q + (long)(t.tok0 + i) * a.qt + (long)(kvh * G + j) * a.qh;
-        float v[F::KS][8];
-        float top = 0.f;
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = mt * 16 + n;
+            live[mt] = r < t.rows;
+            const int i = (t.row0 + (live[mt] ? r : 0)) / G, j = (t.row0 + (live[mt] ? r : 0)) % G;
+            seen_range(t, i, a.causal, a.window, &row_lo[mt], &row_hi[mt]);
+            const T *src = (const T *)a.q + (long)(t.tok0 + i) * a.qt + (long)(kvh * G + j) * a.qh;
 #pragma unroll
-        for (int s = 0; s < F::KS; ++s) {
-            // step s: load s / spl of the K row, part s % spl of the lane's run
-            constexpr int run = F::LB * F::EPB2 / 2, spl = run / 8;
-            const int d0 = (s / spl) * 4 * run + g * run + (s % spl) * 8;
-            float u[8];
-            if (vec) {
-                load_vec<T, 8>(src + d0, u);
-            } else {
+            for (int s = 0; s < F::KS; ++s) {
+                // step s: load s / spl of the K row, part s % spl of the lane's run
+                constexpr int run = F::LB * F::EPB2 / 2, spl = run / 8;
+                const int d0 = (s / spl) * 4 * run + g * run + (s % spl) * 8;
+                if (vec) {
+                    load_vec<T, 8>(src + d0, qv[mt][s]);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = (float)src[d0 + e];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[s][e] = live ? u[k_order<KIND>(e)] : 0.f;
-                top = fmaxf(top, fabsf(v[s][e]));
-            }
-        }
-        const int e = head_room(row_max<4>(top));
-        // the scale's sign goes to q, and a scale of zero too, so that rs > 0 and -inf * rs stays -inf
-        const float up = a.scale < 0.f ? -pow2(e) : a.scale == 0.f ? 0.f : pow2(e);
-        rs[mt] = fmaxf(fabsf(a.scale) * kLog2e * pow2(-e), 0x1p-126f);
-#pragma unroll
-        for (int s = 0; s < F::KS; ++s) {
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float x0 = v[s][2 * k] * up, x1 = v[s][2 * k + 1] * up;
-                h[k] = pack_half(x0, x1);
-                if (P == 2) {
-                    const f16x2 y = __builtin_bit_cast(f16x2, h[k]);
-                    l[k] = pack_half(x0 - (float)y.x, x1 - (float)y.y);
+                    for (int e = 0; e < 8; ++e) qv[mt][s][e] = (float)src[d0 + e];
                 }
             }
-            q[mt][s][0] = join4(h);
-            if (P == 2) q[mt][s][P - 1] = join4(l);
         }
-    }
+    };
+    float rs[MT];
+    f16x8 q[MT][F::KS][P];
+    auto open_q = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top = 0.f;
+#pragma unroll
+            for (int s = 0; s < F::KS; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    qv[mt][s][e] = live[mt] ? qv[mt][s][e] : 0.f;
+                    top = fmaxf(top, fabsf(qv[mt][s][e]));
+                }
+            const int e = head_room(row_max<4>(top));
+            // the scale's sign goes to q, and a scale of zero too, so that rs > 0 and -inf * rs stays -inf
+            const float up = a.scale < 0.f ? -pow2(e) : a.scale == 0.f ? 0.f : pow2(e);
+            rs[mt] = fmaxf(fabsf(a.scale) * kLog2e * pow2(-e), 0x1p-126f);
+#pragma unroll
+            for (int s = 0; s < F::KS; ++s) {
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x0 = qv[mt][s][k_order<KIND>(2 * k)] * up, x1 = qv[mt][s][k_order<KIND>(2 * k + 1)] * up;
+                    h[k] = pack_half(x0, x1);
+                    if (P == 2) {
+                        const f16x2 y = __builtin_bit_cast(f16x2, h[k]);
+                        l[k] = pack_half(x0 - (float)y.x, x1 - (float)y.y);
+                    }
+                }
+                q[mt][s][0] = join4(h);
+                if (P == 2) q[mt][s][P - 1] = join4(l);
+            }
+        }
+    };
 
     const OpenConst oc;
     Meta &meta = sh.meta[wave];
@@ -189,23 +198,31 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
         for (int d = 0; d < F::DT; ++d) o[mt][d] = f32x4{0, 0, 0, 0};
     }
 
+    // the chain q_start -> table -> rows is what a short call waits for: q comes beside it and is opened last
     int i = blk0 + wave;
     uint64_t mask0 = 0, mask1 = 0;
     Place next;
-    if (i < blk1) {
-        const Place p0 = place(look(i));
-        next = place(look(i + 4));
+    {
+        const Key k0 = look(i), k1 = look(i + 4);
+        load_q();
+        const Place p0 = place(k0);
+        next = place(k1);
+        mask0 = p0.mask;
+        mask1 = next.mask;
         if (lane < TK) {
             meta.off[0][lane] = p0.row;
             meta.off[1][lane] = next.row;
-            meta.ks[0][lane] = p0.ok ? ksp[p0.scale] : 0.f;
-            meta.vs[0][lane] = p0.ok ? vsp[p0.scale] : 0.f;
         }
-        mask0 = p0.mask;
-        mask1 = next.mask;
+        const float ks0 = ksp[p0.scale], vs0 = vsp[p0.scale];
         fence();
         load_k(0);
         load_v(0);
+        open_q();
+        if (lane < TK) {
+            meta.ks[0][lane] = p0.ok ? ks0 : 0.f;
+            meta.vs[0][lane] = p0.ok ? vs0 : 0.f;
+        }
+        fence();
     }
     for (int buf = 0; i < blk1; i += 4, buf ^= 1) {
         // in flight through this block: scales of the next, pages of the one after
@@ -260,15 +277,13 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
             const uint64_t own = mask0 >> (4 * g);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const int from = row_lo[mt] - t0 - 4 * g, to = row_hi[mt] - t0 - 4 * g;
+                const uint64_t sees = seen_bits(own, row_lo[mt] - t0 - 4 * g, row_hi[mt] - t0 - 4 * g);
 #pragma unroll
                 for (int kb = 0; kb < F::KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int k = kb * 16 + r;
-                        const bool on = (own >> k & 1) && k >= from && k < to;
-                        s[mt][kb][r] = on ? s[mt][kb][r] : -INFINITY;
-                        vsc[mt][kb][r] = on ? vsc[mt][kb][r] : 0.f;
+                        s[mt][kb][r] = where_seen(sees, kb * 16 + r, s[mt][kb][r], -INFINITY);
+                        vsc[mt][kb][r] = where_seen(sees, kb * 16 + r, vsc[mt][kb][r], 0.f);
                     }
             }
         }
@@ -285,7 +300,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                     if (!F::BF) big = fmaxf(big, fabsf(vsc[mt][kb][r]));
                 }
             m[mt] = fmaxf(m[mt], row_max<4>(top) * rs[mt]);
-            if (!F::BF) e_min[mt] = fminf(e_min[mt], scale_room(row_max<4>(big)));
+            if (!F::BF) e_min[mt] = fminf(e_min[mt], scale_room(row_max<4>(big), 14));
             const float was = ref[mt];
             ref[mt] = m[mt] == -INFINITY ? -INFINITY : m[mt] - e_min[mt];
             const float base = m[mt] == -INFINITY ? 0.f : ref[mt];

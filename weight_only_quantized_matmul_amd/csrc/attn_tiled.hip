@@ -2,10 +2,10 @@
 // tokens): the cache's tiles are opened once into LDS and shared by the rows.
 //
 // A block of NW waves takes a tile of RW * NW rows and walks the positions in
-// steps of TK = 64. K goes to LDS as f16 rows, V transposed, so both are read
-// back as whole 16-byte operands; the next step's codes are in flight from HBM
-// or L2 meanwhile, and two LDS buffers leave one barrier a step. Per step a
-// wave computes for its RW rows
+// steps of TK. K goes to LDS as f16 rows, V transposed, so both are read back
+// as whole 16-byte operands; the next steps' codes are in flight from HBM or L2
+// meanwhile, and three buffers of K and two of V leave one barrier a step. Per
+// step a wave computes for its RW rows
 //     S^T[key][row]  = sum_d K[key][d] Q[row][d]           (A = K, B = Q)
 //     O^T[d][row]   += sum_key V^T[d][key] P^T[key][row]   (A = V^T, B = P^T)
 // with v_mfma_f32_32x32x16 (RW = 32) or 16x16x32 (RW = 16: rows of 256
@@ -13,6 +13,11 @@
 // holds quads of four consecutive keys of one row in S^T; V's columns stand in
 // LDS in the order in which these quads form P^T operands, so probabilities
 // never leave their lane. Parts and scales are as in the few-rows kernel.
+//
+// With eight waves two share a SIMD. The first four do S^T of step t, its
+// softmax and O^T between barriers t and t + 1, the others the softmax of step
+// t, O^T and then S^T of step t + 1: while one runs matrix operations the other
+// has vector work, where in the same order both would wait for the same unit.
 #include "attn_common.h"
 
 namespace wq {
@@ -41,10 +46,11 @@ struct Mma<16> {
 
 template <typename T, int KIND, int D, int NW>
 struct Tiled {
-    static constexpr int RW = D == 256 ? 16 : 32;    // rows a wave
-    static constexpr int TK = 64, NT = 64 * NW, R = RW * NW;
+    static constexpr int RW = tiled_rows(D, sizeof(T) == 4); // rows a wave
+    static constexpr int TK = D == 256 ? 32 : 64;    // positions a step (LDS: 5 buffers of TK * D halves)
+    static constexpr int NT = 64 * NW, R = RW * NW;
     static constexpr int NG = 64 / RW;               // lanes that share a row
-    static constexpr int CH = D / 8;                 // 16-byte chunks of a K row in LDS
+    static constexpr int CH = D / 8, CV = TK / 8;    // 16-byte chunks of a K row and of a V^T row in LDS
     static constexpr int KS = D / (8 * NG);          // steps of a K operand
     static constexpr int KBN = TK / RW, DB = D / RW; // blocks of S^T and of O^T
     static constexpr int QB = RW * RW / 256;         // quads a lane holds of a block
@@ -55,38 +61,40 @@ struct Tiled {
     static constexpr int PP = BF ? 3 : P;            // parts of p
     static constexpr int KU = TK * CH / NT;          // 8-code units of K a thread brings
     static constexpr int KW = KIND == WQ_KV_F16 ? 4 : KIND == WQ_KV_I8 ? 2 : 1; // words of one
-    static constexpr int VK = TK * 32 / NT;          // keys of V a thread brings, D / 32 codes each
-    static constexpr int VE = D / 32;
+    static constexpr int DG = TK * 32 / NT >= 4 ? 32 : 64; // parts of a V row
+    static constexpr int VK = TK * DG / NT;          // keys of V a thread brings, VE codes each
+    static constexpr int VE = D / DG;
+    // In LDS, rows end with 16 bytes of padding (lanes that read 16 bytes of consecutive rows meet no bank twice),
+    // and V^T's row of element d is row d / VE of group d % VE, groups 256 / VE bytes apart besides: threads write
+    // rows of one group, lanes read rows of all, both without conflicts. An operand is then a lane's base plus a
+    // constant: no address arithmetic, one register.
+    static constexpr int KROW = 16 * (CH + 1), KSIZE = TK * KROW;
+    static constexpr int VROW = 16 * (CV + 1), VGROUP = DG * VROW + 256 / VE, VSIZE = VE * VGROUP;
     static constexpr int VB = KIND == WQ_KV_F16 ? 2 * VE : KIND == WQ_KV_I8 ? VE : VE / 2;
     static constexpr int VW = VB < 4 ? 1 : VB / 4;
 };
 
-// where chunk c of row r stands in LDS, in 16-byte chunks
-template <int CH>
-__device__ __forceinline__ int k_at(int r, int c) { return r * CH + (c ^ (r & (CH < 16 ? 7 : 15))); }
-__device__ __forceinline__ int v_at(int d, int c) { return d * 8 + (c ^ ((d ^ (d >> 2)) & 7)); }
-
 template <typename T, int KIND, int D, int NW, typename OFF>
-__global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, const Partials pt, const int vec) {
+__global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a, const Partials pt, const int vec) {
     typedef Tiled<T, KIND, D, NW> F;
     constexpr int RW = F::RW, NG = F::NG, TK = F::TK, P = F::P;
     typedef typename Mma<RW>::acc acc;
-    __shared__ u32x4 sk[2][TK * F::CH];
-    __shared__ u32x4 sv[2][D * 8];
-    __shared__ OFF s_off[2][TK];
+    __shared__ __align__(16) uint8_t sk[3 * F::KSIZE];
+    __shared__ __align__(16) uint8_t sv[2 * F::VSIZE];
+    __shared__ OFF s_off[4][TK];
     __shared__ float s_ks[2][TK], s_vs[2][TK], s_big[2];
-    __shared__ uint64_t s_mask[2];
+    __shared__ uint64_t s_mask[4];
     __shared__ int s_bad[3]; // of step i at i % 3: set a step before its use, cleared a step after
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & (RW - 1), g = lane / RW;
     const int G = a.H / a.c.heads;
     const int kvh = blockIdx.x % a.c.heads;
-    const long rest = blockIdx.x / a.c.heads;
-    const int split = (int)(rest % pt.nsplit);
-    // later tiles see more positions (causal): they start first
-    const long ids = tile_count(a.b.T, G, F::R, a.b.B);
-    const Tile t = find_tile<F::R>(a.b, a.c.page, G, ids - 1 - rest / pt.nsplit, lane);
+    // heads, then tiles, then splits: neighbours have equal work. Blocks go to the shader engines in turn, and where
+    // every other one is short or empty half the engines would get all the work.
+    const long rest = blockIdx.x / a.c.heads, tiles = tile_count(a.b.T, G, F::R, a.b.B);
+    const int split = (int)(rest / tiles);
+    const Tile t = find_tile<F::R>(a.b, a.c.page, G, rest % tiles, lane);
     if (t.rows == 0) return;
     int lo, hi, lo_max, hi_min;
     seen_range(t, t.row0 / G, a.causal, a.window, &lo, &hi_min);
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
     auto look = [&](int i) {
         Key k;
         const int pos = sp.base + i * TK + lane;
-        k.there = i < blk1 && pos >= lo && pos < hi;
+        k.there = i < blk1 && (TK == 64 || lane < TK) && pos >= lo && pos < hi;
         const int idx = page_index(a.c, pos);
         k.slot = pos - idx * a.c.page;
         k.page = k.there ? table[idx] : -1;
@@ -190,33 +198,35 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
     };
     auto put_scales = [&](int buf, bool ok, float ks, float vs) {
         vs = ok ? vs : 0.f;
-        s_ks[buf][lane] = ok ? ks : 0.f;
-        s_vs[buf][lane] = vs;
+        if (TK == 64 || lane < TK) {
+            s_ks[buf][lane] = ok ? ks : 0.f;
+            s_vs[buf][lane] = vs;
+        }
         if (!F::BF) {
-            float big = fabsf(vs);
-#pragma unroll
-            for (int m = 32; m > 0; m >>= 1) big = fmaxf(big, __shfl_xor(big, m));
+            const float big = wave_max(fabsf(vs));
             if (lane == 0) s_big[buf] = big;
         }
     };
 
     // A thread's share of a step: KU units of K, VK keys of V.
     uint32_t rk[F::KU][F::KW], rv[F::VK][F::VW];
-    const int dg = tid & 31, hc = tid >> 5;
+    const int dg = tid & (F::DG - 1), hc = tid / F::DG;
     const int vc = F::VK == 8 ? hc : hc >> 1; // its chunk of V^T: keys v0 .. v0+3 and (VK = 8) v0 + 4 NG .. + 3
     const int v0 = (vc / NG) * 8 * NG + (vc % NG) * 4 + (F::VK == 8 ? 0 : (hc & 1) * 4 * NG);
-    auto fetch = [&](int buf) {
+    auto fetch_k = [&](const OFF *off) {
 #pragma unroll
         for (int u = 0; u < F::KU; ++u) {
             const int x = u * F::NT + tid;
-            load_words<4 * F::KW>(kp + (s_off[buf][x / F::CH] + (OFF)((x % F::CH) * 4 * F::KW)), rk[u]);
+            load_words<4 * F::KW>(kp + (off[x / F::CH] + (OFF)((x % F::CH) * 4 * F::KW)), rk[u]);
         }
+    };
+    auto fetch_v = [&](const OFF *off) {
 #pragma unroll
         for (int k = 0; k < F::VK; ++k)
-            load_words<F::VB>(vp + (s_off[buf][v0 + (k & 3) + (k >> 2) * 4 * NG] + (OFF)(dg * F::VB)), rv[k]);
+            load_words<F::VB>(vp + (off[v0 + (k & 3) + (k >> 2) * 4 * NG] + (OFF)(dg * F::VB)), rv[k]);
     };
-    // ... opened into LDS. `edge`: some rows see less than others or not every position is there.
-    auto store = [&](int buf, int step, uint64_t mask, bool edge) {
+    // ... opened into LDS
+    auto store_k = [&](int buf) {
 #pragma unroll
         for (int u = 0; u < F::KU; ++u) {
             const int x = u * F::NT + tid;
@@ -230,8 +240,11 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
             } else {
                 open_i4(oc, rk[u][0], w);
             }
-            sk[buf][k_at<F::CH>(x / F::CH, x % F::CH)] = u32x4{w[0], w[1], w[2], w[3]};
+            *reinterpret_cast<u32x4 *>(sk + buf * F::KSIZE + x / F::CH * F::KROW + x % F::CH * 16) = u32x4{w[0], w[1], w[2], w[3]};
         }
+    };
+    // `edge`: some rows see less than others or not every position is there.
+    auto store_v = [&](int buf, int step, uint64_t mask, bool edge) {
         if constexpr (KIND == WQ_KV_F16) {
             // An infinity or a NaN among the codes must not reach rows that do not see it (0 * NaN):
             // where rows differ in what they see, such codes leave the operands and are taken one by one.
@@ -283,99 +296,144 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
         }
 #pragma unroll
         for (int e = 0; e < F::VE; ++e) {
-            const int d = dg * F::VE + e;
+            uint8_t *at = sv + buf * F::VSIZE + e * F::VGROUP + dg * F::VROW + vc * 16;
             if constexpr (F::VK == 8)
-                sv[buf][v_at(d, vc)] = u32x4{o[e][0], o[e][1], o[e][2], o[e][3]};
+                *reinterpret_cast<u32x4 *>(at) = u32x4{o[e][0], o[e][1], o[e][2], o[e][3]};
             else
-                reinterpret_cast<u32x2 *>(&sv[buf][v_at(d, vc)])[hc & 1] = u32x2{o[e][0], o[e][1]};
+                *reinterpret_cast<u32x2 *>(at + (hc & 1) * 8) = u32x2{o[e][0], o[e][1]};
         }
     };
-    constexpr uint64_t all = ~0ull;
+    constexpr uint64_t all = TK == 64 ? ~0ull : 0xffffffffull;
     auto is_edge = [&](int i, uint64_t mask) {
         const int t0 = sp.base + i * TK;
         return mask != all || t0 < lo_max || t0 + TK > hi_min;
     };
 
     float ref = -INFINITY, m = -INFINITY, l = 0.f; // p = 2^(s - ref)
-    float e_min = F::BF ? 0.f : 127.f;             // ref = m - e_min: 2^e_min brings the values' scales below 2^14
+    // ref = m - e_min: 2^e_min brings the values' scales below 2^14. A row's sums are rescaled only when its maximum
+    // has grown by more than SLACK powers of two since: all rows of a wave wait when one of them does, and among 32
+    // rows one's maximum moves in most steps of a start. f16 parts leave little room for it above (2^16) or below.
+    constexpr float SLACK = F::BF ? 8.f : F::PP == 1 ? 1.f : 0.f;
+    float e_min = F::BF ? 0.f : 127.f;
     acc o[F::DB];
 #pragma unroll
     for (int d = 0; d < F::DB; ++d)
 #pragma unroll
         for (int k = 0; k < 4 * F::QB; ++k) o[d][k] = 0.f;
 
-    // fill: offsets of steps blk0 and blk0 + 1, codes and scales of blk0
-    Place next;
+    // Operands are read from LDS a fixed number of matrix operations ahead and the order is pinned: left to
+    // itself the scheduler puts every read right before its use, and each operation waits out the LDS's latency.
+    constexpr int KAHEAD = P == 1 ? 6 : 4, VAHEAD = F::PP == 1 ? 6 : F::PP == 2 ? 4 : 3;
+    const int k_lane = n * F::KROW + g * 16, v_lane = n % F::VE * F::VGROUP + n / F::VE * F::VROW + g * 16;
+    acc s[F::KBN];
+    auto scores = [&](int k3, auto beside) { // S^T from K buffer k3; beside(0 .. NQ - 1) as reads end
+        constexpr int N = F::KBN * F::KS;
+        f16x8 fr[KAHEAD];
+        const uint8_t *from = sk + k3 * F::KSIZE + k_lane;
+        auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::KBN * RW * F::KROW + x / F::KBN * NG * 16); };
+#pragma unroll
+        for (int x = 0; x < KAHEAD; ++x) fr[x] = read(x);
+#pragma unroll
+        for (int kb = 0; kb < F::KBN; ++kb)
+#pragma unroll
+            for (int k = 0; k < 4 * F::QB; ++k) s[kb][k] = 0.f;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) s[x % F::KBN] = Mma<RW>::f16(fr[x % KAHEAD], q[x / F::KBN][k], s[x % F::KBN]);
+            if (x + KAHEAD < N) {
+                fr[x % KAHEAD] = read(x + KAHEAD);
+            } else {
+                constexpr int PER = (F::NQ + KAHEAD - 1) / KAHEAD;
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                    if ((x + KAHEAD - N) * PER + k < F::NQ) beside((x + KAHEAD - N) * PER + k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // does the wave work on step i?
+    auto active = [&](int i) { return working && i < blk1 && sp.base + i * TK < w_hi && sp.base + i * TK + TK > w_lo; };
+
+    // Step t of this split works on block blk0 + t. Before barrier 0: K of steps 0 and 1, V and scales of step 0,
+    // offsets of steps 0 to 2.
+    Place place1, place2, place3; // of steps t + 1, t + 2, t + 3 (wave 0)
     if (wave == 0) {
         const Place p0 = place(look(blk0));
-        next = place(look(blk0 + 1));
-        s_off[0][lane] = p0.row;
-        s_off[1][lane] = next.row;
+        place1 = place(look(blk0 + 1));
+        place2 = place(look(blk0 + 2));
+        if (TK == 64 || lane < TK) {
+            s_off[0][lane] = p0.row;
+            s_off[1][lane] = place1.row;
+            s_off[2][lane] = place2.row;
+        }
         put_scales(0, p0.ok, ksp[p0.scale], vsp[p0.scale]);
         if (lane == 0) {
             s_mask[0] = p0.mask;
-            s_mask[1] = next.mask;
+            s_mask[1] = place1.mask;
+            s_mask[2] = place2.mask;
             s_bad[0] = s_bad[1] = s_bad[2] = 0;
         }
     }
     __syncthreads();
     if (blk1 > blk0) {
-        fetch(0);
-        store(0, 0, s_mask[0], is_edge(blk0, s_mask[0]));
+        fetch_k(s_off[0]);
+        fetch_v(s_off[0]);
+        store_k(0);
+        fetch_k(s_off[1]);
+        store_v(0, 0, s_mask[0], is_edge(blk0, s_mask[0]));
+        store_k(1);
     }
     __syncthreads();
+    const bool ahead = NW == 8 && wave >= 4;
+    if (ahead && active(blk0)) scores(0, [](int) {});
 
-    for (int i = blk0, buf = 0; i < blk1; ++i, buf ^= 1) {
-        const int t0 = sp.base + i * TK;
-        const uint64_t mask = s_mask[buf], mask_next = s_mask[buf ^ 1];
-        fetch(buf ^ 1); // past the last step: row 0 again, unused
-        Key after;
+    for (int i = blk0, k3 = 0; i < blk1; ++i) {
+        const int c = i - blk0, buf = c & 1, t0 = sp.base + i * TK;
+        const int k3n = k3 == 2 ? 0 : k3 + 1, k3nn = k3n == 2 ? 0 : k3n + 1; // K buffers of steps t + 1, t + 2
+        const uint64_t mask = s_mask[c & 3], mask_next = s_mask[(c + 1) & 3];
+        float big = F::BF ? 0.f : s_big[buf];
+        const int bad_now = KIND == WQ_KV_F16 ? s_bad[c % 3] : 0;
+        // the keys' scales, read ahead of their use: here, or beside the last matrix operations of S^T
+        f32x4 ksq[F::NQ];
+        auto read_ks = [&](int j) { ksq[j] = *reinterpret_cast<const f32x4 *>(&s_ks[buf][4 * NG * j + 4 * g]); };
+        if (ahead) {
+#pragma unroll
+            for (int j = 0; j < F::NQ; ++j) read_ks(j);
+        }
+        fetch_k(s_off[(c + 2) & 3]); // past the last step: row 0 again, unused
+        fetch_v(s_off[(c + 1) & 3]);
+        Key key3;
         float ks1 = 0.f, vs1 = 0.f;
         if (wave == 0) {
-            after = look(i + 2);
-            ks1 = ksp[next.scale];
-            vs1 = vsp[next.scale];
+            key3 = look(i + 3);
+            ks1 = ksp[place1.scale];
+            vs1 = vsp[place1.scale];
         }
-        if (working && t0 < w_hi && t0 + TK > w_lo) {
-            acc s[F::KBN];
+        if (!ahead && active(i)) scores(k3, read_ks);
+        if (active(i)) {
 #pragma unroll
-            for (int kb = 0; kb < F::KBN; ++kb) {
+            for (int j = 0; j < F::NQ; ++j)
 #pragma unroll
-                for (int k = 0; k < 4 * F::QB; ++k) s[kb][k] = 0.f;
+                for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] *= ksq[j][e];
+            f32x4 vsq[F::NQ];
 #pragma unroll
-                for (int st = 0; st < F::KS; ++st) {
-                    const f16x8 kf = __builtin_bit_cast(f16x8, sk[buf][k_at<F::CH>(kb * RW + n, st * NG + g)]);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) s[kb] = Mma<RW>::f16(kf, q[st][k], s[kb]);
-                }
-            }
-            float vsc[F::NQ][4];
-#pragma unroll
-            for (int j = 0; j < F::NQ; ++j) {
-                const f32x4 ks = *reinterpret_cast<const f32x4 *>(&s_ks[buf][4 * NG * j + 4 * g]);
-                const f32x4 vs = *reinterpret_cast<const f32x4 *>(&s_vs[buf][4 * NG * j + 4 * g]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[j / F::QB][4 * (j % F::QB) + e] *= ks[e];
-                    vsc[j][e] = vs[e];
-                }
-            }
-            float big = s_big[buf];
+            for (int j = 0; j < F::NQ; ++j) vsq[j] = *reinterpret_cast<const f32x4 *>(&s_vs[buf][4 * NG * j + 4 * g]);
+            __builtin_amdgcn_sched_barrier(0);
             const bool edge = mask != all || t0 < w_lo_max || t0 + TK > w_hi_min;
-            if (edge) { // a key that a row does not see scores -inf there and has scale 0, whatever it held
-                const uint64_t own = mask >> (4 * g);
-                const int from = row_lo - t0 - 4 * g, to = row_hi - t0 - 4 * g;
+            // the lane's row sees key 4 g + k of the step: bit k
+            const uint64_t sees = seen_bits(mask >> (4 * g), row_lo - t0 - 4 * g, row_hi - t0 - 4 * g);
+            if (edge) { // a key that a row does not see scores -inf there
                 big = 0.f;
 #pragma unroll
-                for (int j = 0; j < F::NQ; ++j)
+                for (int j = 0; j < F::NQ; ++j) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int k = 4 * NG * j + e;
-                        const bool on = (own >> k & 1) && k >= from && k < to;
-                        s[j / F::QB][4 * (j % F::QB) + e] = on ? s[j / F::QB][4 * (j % F::QB) + e] : -INFINITY;
-                        vsc[j][e] = on ? vsc[j][e] : 0.f;
-                        big = fmaxf(big, fabsf(vsc[j][e]));
+                        s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], -INFINITY);
+                        if (!F::BF) big = fmaxf(big, fabsf(where_seen(sees, 4 * NG * j + e, vsq[j][e], 0.f)));
                     }
+                }
                 if (!F::BF) big = row_max<NG>(big);
             }
             float top = -INFINITY;
@@ -383,28 +441,40 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
             for (int j = 0; j < F::NQ; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j / F::QB][4 * (j % F::QB) + e]);
-            m = fmaxf(m, row_max<NG>(top) * rs);
-            if (!F::BF) e_min = fminf(e_min, scale_room(big));
-            const float was = ref;
-            ref = m == -INFINITY ? -INFINITY : m - e_min;
+            const float now = row_max<NG>(top) * rs;
+            float grow = 1.f;
+            const float room = F::BF ? 0.f : fminf(e_min, scale_room(big, 14));
+            // rows that move: the maximum has left the slack, or a value's scale its room (or is not a number)
+            const bool moves = !(now <= m + SLACK) || room < e_min;
+            if (__ballot(moves)) {
+                const float was = ref;
+                m = moves ? fmaxf(m, now) : m;
+                e_min = moves ? room : e_min;
+                ref = m == -INFINITY ? -INFINITY : m - e_min;
+                grow = __builtin_amdgcn_exp2f(was - (m == -INFINITY ? 0.f : ref));
+#pragma unroll
+                for (int d = 0; d < F::DB; ++d) o[d] *= grow;
+            }
             const float base = m == -INFINITY ? 0.f : ref;
-            const float grow = __builtin_amdgcn_exp2f(was - base);
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < F::NQ; ++j)
+            for (int j = 0; j < F::NQ; ++j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float p = __builtin_amdgcn_exp2f(fmaf(s[j / F::QB][4 * (j % F::QB) + e], rs, -base));
                     sum += p;
-                    s[j / F::QB][4 * (j % F::QB) + e] = p * vsc[j][e];
+                    s[j / F::QB][4 * (j % F::QB) + e] = p * vsq[j][e];
                 }
-            l = l * grow + sum;
-            if (__ballot(grow != 1.f)) {
-#pragma unroll
-                for (int d = 0; d < F::DB; ++d) o[d] *= grow;
             }
+            if (edge) { // ... and takes no part of the value, whatever its scale (0 * NaN)
+#pragma unroll
+                for (int j = 0; j < F::NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], 0.f);
+            }
+            l = l * grow + sum;
             if constexpr (KIND == WQ_KV_F16) {
-                if (s_bad[(i - blk0) % 3]) {
+                if (bad_now) {
                     for (int key = 0; key < TK; ++key) {
                         if (!(mask >> key & 1)) continue;
                         // the row's offset is no longer in LDS: look it up again
@@ -429,6 +499,12 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
                     }
                 }
             }
+            constexpr int N = F::ST * F::DB;
+            f16x8 fr[VAHEAD];
+            const uint8_t *from = sv + buf * F::VSIZE + v_lane;
+            auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::DB * (RW / F::VE) * F::VROW + x / F::DB * NG * 16); };
+#pragma unroll
+            for (int x = 0; x < VAHEAD; ++x) fr[x] = read(x);
 #pragma unroll
             for (int st = 0; st < F::ST; ++st) {
                 uint32_t pb[F::PP][4];
@@ -450,23 +526,31 @@ __global__ __launch_bounds__(64 * NW) void attn_tiled_kernel(const AttnArgs a, c
                         }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int d = 0; d < F::DB; ++d) {
-                    const f16x8 vf = __builtin_bit_cast(f16x8, sv[buf][v_at(d * RW + n, st * NG + g)]);
+                    const int x = st * F::DB + d;
 #pragma unroll
-                    for (int k = 0; k < F::PP; ++k) o[d] = F::BF ? Mma<RW>::bf16(vf, join4(pb[k]), o[d]) : Mma<RW>::f16(vf, join4(pb[k]), o[d]);
+                    for (int k = 0; k < F::PP; ++k)
+                        o[d] = F::BF ? Mma<RW>::bf16(fr[x % VAHEAD], join4(pb[k]), o[d]) : Mma<RW>::f16(fr[x % VAHEAD], join4(pb[k]), o[d]);
+                    if (x + VAHEAD < N) fr[x % VAHEAD] = read(x + VAHEAD);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        if (KIND == WQ_KV_F16 && tid == 0) s_bad[(i - blk0 + 2) % 3] = 0;
-        store(buf ^ 1, i + 1 - blk0, mask_next, is_edge(i + 1, mask_next));
+        if (ahead && active(i + 1)) scores(k3n, [](int) {});
+        if (KIND == WQ_KV_F16 && tid == 0) s_bad[(c + 2) % 3] = 0;
+        store_k(k3nn);
+        store_v(buf ^ 1, c + 1, mask_next, is_edge(i + 1, mask_next));
         if (wave == 0) {
-            const Place p2 = place(after);
-            put_scales(buf ^ 1, next.ok, ks1, vs1);
-            s_off[buf][lane] = p2.row;
-            if (lane == 0) s_mask[buf] = p2.mask;
-            next = p2;
+            place3 = place(key3);
+            put_scales(buf ^ 1, place1.ok, ks1, vs1);
+            if (TK == 64 || lane < TK) s_off[(c + 3) & 3][lane] = place3.row;
+            if (lane == 0) s_mask[(c + 3) & 3] = place3.mask;
+            place1 = place2;
+            place2 = place3;
         }
+        k3 = k3n;
         __syncthreads();
     }
 

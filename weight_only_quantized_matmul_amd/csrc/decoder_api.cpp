@@ -116,7 +116,7 @@ int kv_copy(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k, void *v
 // How the positions are split: enough waves for every SIMD to have some in
 // flight, but no split shorter than pays for its partial result. Lengths that
 // are not known are taken from the table's width.
-wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int causal, int window, int cus) {
+wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int causal, int window, bool f32, int cus) {
     wq::AttnPlan p;
     const long G = H / c->heads;
     const long q = b->max_q > 0 ? (b->max_q < b->T ? b->max_q : b->T) : ((long)b->T + b->B - 1) / b->B;
@@ -131,10 +131,10 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
         p.step = row <= 128 ? 64 : 32;
     } else {
         // eight waves share each opened tile when their larger tiles still give every CU a block
-        const long wave_rows = c->dim == 256 ? 16 : 32;
+        const long wave_rows = wq::tiled_rows(c->dim, f32);
         if ((q * G + 8 * wave_rows - 1) / (8 * wave_rows) * b->B * c->heads >= cus) p.waves = 8;
         p.rows = (int)wave_rows * p.waves;
-        p.step = 64;
+        p.step = c->dim == 256 ? 32 : 64;
     }
     // tiles that are there (the numbers that whole sequences leave unused not counted), and their steps
     const long tiles = (q * G + p.rows - 1) / p.rows * b->B, numbers = wq::tile_count(b->T, G, p.rows, b->B);
@@ -142,10 +142,10 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     const long total = (tiles < numbers ? tiles : numbers) * c->heads * steps;
     if (p.few) {
         long per_wave = total / (cus * 12);
-        per_wave = per_wave < 1 ? 1 : per_wave > 8 ? 8 : per_wave;
+        per_wave = per_wave < 1 ? 1 : per_wave > 16 ? 16 : per_wave;
         p.least = (int)(4 * per_wave);
     } else {
-        const long per_block = total / (2 * cus);
+        const long per_block = total / (3 * cus);
         p.least = (int)(per_block < 4 ? 4 : per_block > steps ? steps : per_block);
     }
     long n = (steps + p.least - 1) / p.least;
@@ -311,7 +311,7 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
     a.H = H;
     a.causal = causal != 0;
     a.window = window;
-    const wq::AttnPlan p = plan_attn(cache, batch, H, a.causal, window, wq::device_cus(cache->device));
+    const wq::AttnPlan p = plan_attn(cache, batch, H, a.causal, window, dtype == WQ_DT_F32, wq::device_cus(cache->device));
     wq::Partials pt;
     pt.part = pt.ml = nullptr;
     pt.nsplit = p.nsplit;
