@@ -13,11 +13,6 @@
 // holds quads of four consecutive keys of one row in S^T; V's columns stand in
 // LDS in the order in which these quads form P^T operands, so probabilities
 // never leave their lane. Parts and scales are as in the few-rows kernel.
-//
-// With eight waves two share a SIMD. The first four do S^T of step t, its
-// softmax and O^T between barriers t and t + 1, the others the softmax of step
-// t, O^T and then S^T of step t + 1: while one runs matrix operations the other
-// has vector work, where in the same order both would wait for the same unit.
 #include "attn_common.h"
 
 namespace wq {
@@ -56,6 +51,8 @@ struct Tiled {
     static constexpr int QB = RW * RW / 256;         // quads a lane holds of a block
     static constexpr int NQ = KBN * QB;              // quads a lane holds of a step: keys 4 NG q + 4 g + 0..3
     static constexpr int ST = NQ / 2;                // steps of a V operand: quads 2s, 2s + 1
+    static constexpr int HV = RW == 32 ? 2 : 1;      // a step is taken in so many parts (registers)
+    static constexpr int KBH = KBN / HV, NQH = NQ / HV, STH = ST / HV;
     static constexpr int P = sizeof(T) == 4 ? 2 : 1; // f16 parts of q
     static constexpr bool BF = P == 2 && KIND != WQ_KV_F16;
     static constexpr int PP = BF ? 3 : P;            // parts of p
@@ -81,7 +78,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     typedef typename Mma<RW>::acc acc;
     __shared__ __align__(16) uint8_t sk[3 * F::KSIZE];
     __shared__ __align__(16) uint8_t sv[2 * F::VSIZE];
-    __shared__ OFF s_off[4][TK];
+    __shared__ OFF s_off[4][TK], s_sc[4][TK]; // rows (bytes) and scales (floats) of a step's positions
     __shared__ float s_ks[2][TK], s_vs[2][TK], s_big[2];
     __shared__ uint64_t s_mask[4];
     __shared__ int s_bad[3]; // of step i at i % 3: set a step before its use, cleared a step after
@@ -196,14 +193,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
         p.mask = __ballot(p.ok);
         return p;
     };
-    auto put_scales = [&](int buf, bool ok, float ks, float vs) {
-        vs = ok ? vs : 0.f;
+    // Bringing a step's places and scales is spread over three waves (0: places, 1: keys' scales, 2: values' scales):
+    // the others wait at the barrier for the slowest.
+    auto put_place = [&](int slot, const Place &p) {
         if (TK == 64 || lane < TK) {
-            s_ks[buf][lane] = ok ? ks : 0.f;
-            s_vs[buf][lane] = vs;
+            s_off[slot][lane] = p.row;
+            s_sc[slot][lane] = p.scale;
         }
-        if (!F::BF) {
-            const float big = wave_max(fabsf(vs));
+        if (lane == 0) s_mask[slot] = p.mask;
+    };
+    auto get_scale = [&](int slot) {
+        const OFF at = s_sc[slot][lane & (TK - 1)];
+        return wave == 1 ? ksp[at] : vsp[at];
+    };
+    auto put_scale = [&](int buf, int slot, float x) {
+        x = s_mask[slot] >> lane & 1 ? x : 0.f;
+        if (TK == 64 || lane < TK) (wave == 1 ? s_ks : s_vs)[buf][lane] = x;
+        if (!F::BF && wave == 2) {
+            const float big = wave_max(fabsf(x));
             if (lane == 0) s_big[buf] = big;
         }
     };
@@ -323,32 +330,34 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
 
     // Operands are read from LDS a fixed number of matrix operations ahead and the order is pinned: left to
     // itself the scheduler puts every read right before its use, and each operation waits out the LDS's latency.
-    constexpr int KAHEAD = P == 1 ? 6 : 4, VAHEAD = F::PP == 1 ? 6 : F::PP == 2 ? 4 : 3;
+    constexpr int KN = F::KBH * F::KS, VN = F::STH * F::DB; // operands of a part
+    constexpr int KWANT = P == 1 ? 6 : 4, VWANT = F::PP == 1 ? 6 : F::PP == 2 ? 4 : 3;
+    constexpr int KAHEAD = KWANT < KN ? KWANT : KN, VAHEAD = VWANT < VN ? VWANT : VN;
     const int k_lane = n * F::KROW + g * 16, v_lane = n % F::VE * F::VGROUP + n / F::VE * F::VROW + g * 16;
-    acc s[F::KBN];
-    auto scores = [&](int k3, auto beside) { // S^T from K buffer k3; beside(0 .. NQ - 1) as reads end
-        constexpr int N = F::KBN * F::KS;
+    acc s[F::KBH];
+    auto scores = [&](int k3, int h, auto beside) { // S^T of part h from K buffer k3; beside(0 .. NQH - 1) as reads end
+        constexpr int N = KN;
         f16x8 fr[KAHEAD];
-        const uint8_t *from = sk + k3 * F::KSIZE + k_lane;
-        auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::KBN * RW * F::KROW + x / F::KBN * NG * 16); };
+        const uint8_t *from = sk + k3 * F::KSIZE + h * F::KBH * RW * F::KROW + k_lane;
+        auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::KBH * RW * F::KROW + x / F::KBH * NG * 16); };
 #pragma unroll
         for (int x = 0; x < KAHEAD; ++x) fr[x] = read(x);
 #pragma unroll
-        for (int kb = 0; kb < F::KBN; ++kb)
+        for (int kb = 0; kb < F::KBH; ++kb)
 #pragma unroll
             for (int k = 0; k < 4 * F::QB; ++k) s[kb][k] = 0.f;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int x = 0; x < N; ++x) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) s[x % F::KBN] = Mma<RW>::f16(fr[x % KAHEAD], q[x / F::KBN][k], s[x % F::KBN]);
+            for (int k = 0; k < P; ++k) s[x % F::KBH] = Mma<RW>::f16(fr[x % KAHEAD], q[x / F::KBH][k], s[x % F::KBH]);
             if (x + KAHEAD < N) {
                 fr[x % KAHEAD] = read(x + KAHEAD);
             } else {
-                constexpr int PER = (F::NQ + KAHEAD - 1) / KAHEAD;
+                constexpr int PER = (F::NQH + KAHEAD - 1) / KAHEAD;
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if ((x + KAHEAD - N) * PER + k < F::NQ) beside((x + KAHEAD - N) * PER + k);
+                    if ((x + KAHEAD - N) * PER + k < F::NQH) beside((x + KAHEAD - N) * PER + k);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -358,25 +367,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
 
     // Step t of this split works on block blk0 + t. Before barrier 0: K of steps 0 and 1, V and scales of step 0,
     // offsets of steps 0 to 2.
-    Place place1, place2, place3; // of steps t + 1, t + 2, t + 3 (wave 0)
     if (wave == 0) {
-        const Place p0 = place(look(blk0));
-        place1 = place(look(blk0 + 1));
-        place2 = place(look(blk0 + 2));
-        if (TK == 64 || lane < TK) {
-            s_off[0][lane] = p0.row;
-            s_off[1][lane] = place1.row;
-            s_off[2][lane] = place2.row;
-        }
-        put_scales(0, p0.ok, ksp[p0.scale], vsp[p0.scale]);
-        if (lane == 0) {
-            s_mask[0] = p0.mask;
-            s_mask[1] = place1.mask;
-            s_mask[2] = place2.mask;
-            s_bad[0] = s_bad[1] = s_bad[2] = 0;
-        }
+        const Key k0 = look(blk0), k1 = look(blk0 + 1), k2 = look(blk0 + 2);
+        put_place(0, place(k0));
+        put_place(1, place(k1));
+        put_place(2, place(k2));
+        if (lane == 0) s_bad[0] = s_bad[1] = s_bad[2] = 0;
     }
     __syncthreads();
+    if (wave == 1 || wave == 2) put_scale(0, 0, get_scale(0));
     if (blk1 > blk0) {
         fetch_k(s_off[0]);
         fetch_v(s_off[0]);
@@ -386,59 +385,53 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
         store_k(1);
     }
     __syncthreads();
-    const bool ahead = NW == 8 && wave >= 4;
-    if (ahead && active(blk0)) scores(0, [](int) {});
 
     for (int i = blk0, k3 = 0; i < blk1; ++i) {
         const int c = i - blk0, buf = c & 1, t0 = sp.base + i * TK;
         const int k3n = k3 == 2 ? 0 : k3 + 1, k3nn = k3n == 2 ? 0 : k3n + 1; // K buffers of steps t + 1, t + 2
         const uint64_t mask = s_mask[c & 3], mask_next = s_mask[(c + 1) & 3];
-        float big = F::BF ? 0.f : s_big[buf];
+        const float big_all = F::BF ? 0.f : s_big[buf];
         const int bad_now = KIND == WQ_KV_F16 ? s_bad[c % 3] : 0;
-        // the keys' scales, read ahead of their use: here, or beside the last matrix operations of S^T
-        f32x4 ksq[F::NQ];
-        auto read_ks = [&](int j) { ksq[j] = *reinterpret_cast<const f32x4 *>(&s_ks[buf][4 * NG * j + 4 * g]); };
-        if (ahead) {
-#pragma unroll
-            for (int j = 0; j < F::NQ; ++j) read_ks(j);
-        }
         fetch_k(s_off[(c + 2) & 3]); // past the last step: row 0 again, unused
         fetch_v(s_off[(c + 1) & 3]);
         Key key3;
-        float ks1 = 0.f, vs1 = 0.f;
-        if (wave == 0) {
-            key3 = look(i + 3);
-            ks1 = ksp[place1.scale];
-            vs1 = vsp[place1.scale];
-        }
-        if (!ahead && active(i)) scores(k3, read_ks);
+        float scale1 = 0.f;
+        if (wave == 0) key3 = look(i + 3);
+        if (wave == 1 || wave == 2) scale1 = get_scale((c + 1) & 3);
         if (active(i)) {
 #pragma unroll
-            for (int j = 0; j < F::NQ; ++j)
+        for (int h = 0; h < F::HV; ++h) {
+            f32x4 ksq[F::NQH], vsq[F::NQH]; // scales of keys and values, read ahead of their use
+            const float *ks_at = &s_ks[buf][h * (TK / F::HV) + 4 * g], *vs_at = &s_vs[buf][h * (TK / F::HV) + 4 * g];
+            __builtin_amdgcn_s_setprio(1);
+            scores(k3, h, [&](int j) { ksq[j] = *reinterpret_cast<const f32x4 *>(ks_at + 4 * NG * j); });
+            __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+            for (int j = 0; j < F::NQH; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] *= ksq[j][e];
-            f32x4 vsq[F::NQ];
 #pragma unroll
-            for (int j = 0; j < F::NQ; ++j) vsq[j] = *reinterpret_cast<const f32x4 *>(&s_vs[buf][4 * NG * j + 4 * g]);
+            for (int j = 0; j < F::NQH; ++j) vsq[j] = *reinterpret_cast<const f32x4 *>(vs_at + 4 * NG * j);
             __builtin_amdgcn_sched_barrier(0);
+            float big = big_all;
             const bool edge = mask != all || t0 < w_lo_max || t0 + TK > w_hi_min;
-            // the lane's row sees key 4 g + k of the step: bit k
-            const uint64_t sees = seen_bits(mask >> (4 * g), row_lo - t0 - 4 * g, row_hi - t0 - 4 * g);
+            // the lane's row sees key 4 g + k of the part: bit k
+            const uint64_t sees = seen_bits(mask >> (4 * g), row_lo - t0 - 4 * g, row_hi - t0 - 4 * g) >> (h * (TK / F::HV));
             if (edge) { // a key that a row does not see scores -inf there
-                big = 0.f;
+                float most = 0.f;
 #pragma unroll
-                for (int j = 0; j < F::NQ; ++j) {
+                for (int j = 0; j < F::NQH; ++j) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], -INFINITY);
-                        if (!F::BF) big = fmaxf(big, fabsf(where_seen(sees, 4 * NG * j + e, vsq[j][e], 0.f)));
+                        if (!F::BF) most = fmaxf(most, fabsf(where_seen(sees, 4 * NG * j + e, vsq[j][e], 0.f)));
                     }
                 }
-                if (!F::BF) big = row_max<NG>(big);
+                if (!F::BF) big = row_max<NG>(most);
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < F::NQ; ++j)
+            for (int j = 0; j < F::NQH; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, s[j / F::QB][4 * (j % F::QB) + e]);
             const float now = row_max<NG>(top) * rs;
@@ -458,7 +451,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
             const float base = m == -INFINITY ? 0.f : ref;
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < F::NQ; ++j) {
+            for (int j = 0; j < F::NQH; ++j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float p = __builtin_amdgcn_exp2f(fmaf(s[j / F::QB][4 * (j % F::QB) + e], rs, -base));
@@ -468,24 +461,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
             }
             if (edge) { // ... and takes no part of the value, whatever its scale (0 * NaN)
 #pragma unroll
-                for (int j = 0; j < F::NQ; ++j)
+                for (int j = 0; j < F::NQH; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], 0.f);
             }
             l = l * grow + sum;
             if constexpr (KIND == WQ_KV_F16) {
                 if (bad_now) {
-                    for (int key = 0; key < TK; ++key) {
+                    for (int key = h * (TK / F::HV); key < (h + 1) * (TK / F::HV); ++key) {
                         if (!(mask >> key & 1)) continue;
                         // the row's offset is no longer in LDS: look it up again
                         const int pos = t0 + key, idx = page_index(a.c, pos);
                         const f16 *src = (const f16 *)(vp + ((OFF)table[idx] * (OFF)a.c.rp + (OFF)(pos - idx * a.c.page) * (OFF)a.c.rs));
                         float y = 0.f;
 #pragma unroll
-                        for (int j = 0; j < F::NQ; ++j)
+                        for (int j = 0; j < F::NQH; ++j)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (j == key / (4 * NG) && e == (key & 3)) y = s[j / F::QB][4 * (j % F::QB) + e];
+                                if (j == key / (4 * NG) - h * F::NQH && e == (key & 3)) y = s[j / F::QB][4 * (j % F::QB) + e];
                         y = __shfl(y, (key >> 2 & (NG - 1)) * RW + n);
                         if (pos >= row_lo && pos < row_hi) {
 #pragma unroll
@@ -499,14 +492,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
                     }
                 }
             }
-            constexpr int N = F::ST * F::DB;
+            constexpr int N = VN;
+            __builtin_amdgcn_s_setprio(1);
             f16x8 fr[VAHEAD];
-            const uint8_t *from = sv + buf * F::VSIZE + v_lane;
+            const uint8_t *from = sv + buf * F::VSIZE + h * F::STH * NG * 16 + v_lane;
             auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::DB * (RW / F::VE) * F::VROW + x / F::DB * NG * 16); };
 #pragma unroll
             for (int x = 0; x < VAHEAD; ++x) fr[x] = read(x);
 #pragma unroll
-            for (int st = 0; st < F::ST; ++st) {
+            for (int st = 0; st < F::STH; ++st) {
                 uint32_t pb[F::PP][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -536,20 +530,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
                     if (x + VAHEAD < N) fr[x % VAHEAD] = read(x + VAHEAD);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+            __builtin_amdgcn_s_setprio(0);
             }
         }
-        if (ahead && active(i + 1)) scores(k3n, [](int) {});
+        }
         if (KIND == WQ_KV_F16 && tid == 0) s_bad[(c + 2) % 3] = 0;
         store_k(k3nn);
         store_v(buf ^ 1, c + 1, mask_next, is_edge(i + 1, mask_next));
-        if (wave == 0) {
-            place3 = place(key3);
-            put_scales(buf ^ 1, place1.ok, ks1, vs1);
-            if (TK == 64 || lane < TK) s_off[(c + 3) & 3][lane] = place3.row;
-            if (lane == 0) s_mask[(c + 3) & 3] = place3.mask;
-            place1 = place2;
-            place2 = place3;
-        }
+        if (wave == 0) put_place((c + 3) & 3, place(key3));
+        if (wave == 1 || wave == 2) put_scale(buf ^ 1, (c + 1) & 3, scale1);
         k3 = k3n;
         __syncthreads();
     }

@@ -145,8 +145,11 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
         per_wave = per_wave < 1 ? 1 : per_wave > 16 ? 16 : per_wave;
         p.least = (int)(4 * per_wave);
     } else {
-        const long per_block = total / (3 * cus);
-        p.least = (int)(per_block < 4 ? 4 : per_block > steps ? steps : per_block);
+        // a block for every CU: no split (its partial results cost more than the tail they save);
+        // else enough splits for two blocks a CU
+        const long blocks = (tiles < numbers ? tiles : numbers) * c->heads, want = blocks >= cus ? 1 : (2 * cus + blocks - 1) / blocks;
+        p.least = (int)((steps + want - 1) / want);
+        if (p.least < 4) p.least = 4;
     }
     long n = (steps + p.least - 1) / p.least;
     const long rows = (long)b->T * H;
