@@ -22,9 +22,49 @@ struct IsCode<int8_t> {
 // The larger of two non-negative doubles across lanes m apart.
 __device__ __forceinline__ double max_across(double t, int m) { return fmax(t, __shfl_xor(t, m)); }
 
+// VEC elements from p. ANY: p is aligned to its element only and the row may end
+// before them (`left` elements are there; the rest are zeros). The hardware
+// takes wide loads and stores at any address, so odd rows keep them too: only
+// a row's last elements go one by one.
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void load_row(const T *p, int left, float *v) {
+    if constexpr (!ANY) {
+        load_vec<T, VEC>(p, v);
+    } else {
+        typedef T vt __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+        if (left >= VEC) {
+            const vt r = *reinterpret_cast<const vt *>(p);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = (float)r[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = i < left ? (float)p[i] : 0.f;
+        }
+    }
+}
+
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void store_row(T *p, int left, const float *v) {
+    if constexpr (!ANY) {
+        store_vec<T, VEC>(p, v);
+    } else {
+        typedef T vt __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+        if (left >= VEC) {
+            vt r;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) r[i] = (T)v[i];
+            *reinterpret_cast<vt *>(p) = r;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i < left) p[i] = (T)v[i];
+        }
+    }
+}
+
 // VEC elements a load, NV loads a thread: n <= blockDim * NV * VEC. w is read
 // twice (from L2) rather than held: fewer registers, more rows in flight.
-template <typename TX, typename TY, int VEC, int NV>
+template <typename TX, typename TY, int VEC, int NV, bool ANY>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
     constexpr bool CODE = IsCode<TY>::value;
     __shared__ float red[16];
@@ -39,7 +79,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
         const int e = (j * nt + tid) * VEC;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
-        if (e < n) load_vec<TX, VEC>(x + e, v[j]);
+        if (e < n) load_row<TX, VEC, ANY>(x + e, n - e, v[j]);
     }
     if (res) {
         float r[NV][VEC];
@@ -48,7 +88,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
             const int e = (j * nt + tid) * VEC;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) r[j][i] = 0.f;
-            if (e < n) load_vec<TX, VEC>(res + e, r[j]);
+            if (e < n) load_row<TX, VEC, ANY>(res + e, n - e, r[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -69,7 +109,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
             const int e = (j * nt + tid) * VEC;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) w[j][i] = 0.f;
-            if (e < n) load_vec<float, VEC>(a.w + e, w[j]);
+            if (e < n) load_row<float, VEC, ANY>(a.w + e, n - e, w[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -104,7 +144,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int e = (j * nt + tid) * VEC;
-            if (e < n) store_vec<TX, VEC>(s + e, v[j]);
+            if (e < n) store_row<TX, VEC, ANY>(s + e, n - e, v[j]);
         }
     }
     TY *y = (TY *)a.y + row * a.ys;
@@ -114,10 +154,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
             const int e = (j * nt + tid) * VEC;
             if (e < n) {
                 float o[VEC], w[VEC];
-                load_vec<float, VEC>(a.w + e, w);
+                load_row<float, VEC, ANY>(a.w + e, n - e, w);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[i];
-                store_vec<TY, VEC>(y + e, o);
+                store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         }
     } else {
@@ -132,7 +172,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
             const int e = (j * nt + tid) * VEC;
             if (e < n) {
                 float o[VEC], w[VEC];
-                load_vec<float, VEC>(a.w + e, w);
+                load_row<float, VEC, ANY>(a.w + e, n - e, w);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const float f = v[j][i] * w[i] * inv; // within 127 * 4 * 2^-24 of the quotient
@@ -141,13 +181,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
                         c = (float)rint((double)v[j][i] * (double)w[i] * 127.0 / top);
                     o[i] = ok ? c : 0.f;
                 }
-                store_vec<TY, VEC>(y + e, o);
+                store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         }
     }
 }
 
-template <typename TX, typename TY, int VEC>
+template <typename TX, typename TY, int VEC, bool ANY>
 hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     const int chunks = (a.n + VEC - 1) / VEC;
     // With rows for every CU, blocks of 256 threads (several a CU, a long row
@@ -155,9 +195,9 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     // one row is what counts then.
     const int want = a.rows >= 2 * cus ? 256 : 1024;
     constexpr int LAST = 32768 / 1024 / VEC; // loads a thread at the longest row
-    const int sizes[] = {1, 2, 3, 4, 8, 16, 32};
+    const int sizes[] = {1, 2, 3, 4, 8};
     int nv = 1;
-    for (int i = 0; i < 7 && sizes[i] <= LAST; ++i) {
+    for (int i = 0; i < 5 && sizes[i] <= LAST; ++i) {
         nv = sizes[i];
         if ((chunks + nv - 1) / nv <= want) break;
     }
@@ -167,9 +207,9 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     switch (nv) {
 #define WQ_NV(N)                                                                                         \
     case N:                                                                                              \
-        if constexpr (N <= LAST) hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N>), grid, block, 0, st, a); \
+        if constexpr (N <= LAST) hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY>), grid, block, 0, st, a); \
         break;
-        WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8) WQ_NV(16) WQ_NV(32)
+        WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8)
 #undef WQ_NV
     default: return hipErrorInvalidValue;
     }
@@ -180,10 +220,10 @@ template <typename TX>
 hipError_t launch_x(const NormArgs &a, int y_dtype, bool vec, int cus, hipStream_t st) {
     constexpr int V = sizeof(TX) == 4 ? 4 : 8;
     switch (y_dtype) {
-    case WQ_DT_F32: return vec ? launch_nv<TX, float, V>(a, cus, st) : launch_nv<TX, float, 1>(a, cus, st);
-    case WQ_DT_BF16: return vec ? launch_nv<TX, bf16, V>(a, cus, st) : launch_nv<TX, bf16, 1>(a, cus, st);
-    case WQ_DT_F16: return vec ? launch_nv<TX, f16, V>(a, cus, st) : launch_nv<TX, f16, 1>(a, cus, st);
-    default: return vec ? launch_nv<TX, int8_t, V>(a, cus, st) : launch_nv<TX, int8_t, 1>(a, cus, st);
+    case WQ_DT_F32: return vec ? launch_nv<TX, float, V, false>(a, cus, st) : launch_nv<TX, float, V, true>(a, cus, st);
+    case WQ_DT_BF16: return vec ? launch_nv<TX, bf16, V, false>(a, cus, st) : launch_nv<TX, bf16, V, true>(a, cus, st);
+    case WQ_DT_F16: return vec ? launch_nv<TX, f16, V, false>(a, cus, st) : launch_nv<TX, f16, V, true>(a, cus, st);
+    default: return vec ? launch_nv<TX, int8_t, V, false>(a, cus, st) : launch_nv<TX, int8_t, V, true>(a, cus, st);
     }
 }
 
