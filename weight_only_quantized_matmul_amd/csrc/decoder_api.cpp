@@ -142,7 +142,10 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     const long total = (tiles < numbers ? tiles : numbers) * c->heads * steps;
     if (p.few) {
         long per_wave = total / (cus * 12);
-        per_wave = per_wave < 1 ? 1 : per_wave > 16 ? 16 : per_wave;
+        // many sequences differ in length: shorter splits even that out (64 ragged sequences: 150 us with 8 steps a wave,
+        // 155 with 16); few are split for the chip's sake and pay for each split's start (4 long ones: 179 and 154 us)
+        const long most = (tiles < numbers ? tiles : numbers) * c->heads >= cus ? 8 : 16;
+        per_wave = per_wave < 1 ? 1 : per_wave > most ? most : per_wave;
         p.least = (int)(4 * per_wave);
     } else {
         // a block for every CU: no split (its partial results cost more than the tail they save);
