@@ -19,171 +19,172 @@ struct IsCode<int8_t> {
     static constexpr bool value = true;
 };
 
-// The larger of two non-negative doubles across lanes m apart.
-__device__ __forceinline__ double max_across(double t, int m) { return fmax(t, __shfl_xor(t, m)); }
+template <typename T, int VEC>
+struct Vec {
+    typedef T type __attribute__((ext_vector_type(VEC), aligned(VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16)));
+    typedef T any __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+};
 
 // VEC elements from p. ANY: p is aligned to its element only and the row may end
 // before them (`left` elements are there; the rest are zeros). The hardware
 // takes wide loads and stores at any address, so odd rows keep them too: only
 // a row's last elements go one by one.
 template <typename T, int VEC, bool ANY>
-__device__ __forceinline__ void load_row(const T *p, int left, float *v) {
-    if constexpr (!ANY) {
-        load_vec<T, VEC>(p, v);
-    } else {
-        typedef T vt __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
-        if (left >= VEC) {
-            const vt r = *reinterpret_cast<const vt *>(p);
+__device__ __forceinline__ typename Vec<T, VEC>::type load_row(const T *p, int left) {
+    typename Vec<T, VEC>::type v;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = (float)r[i];
-        } else {
+    for (int i = 0; i < VEC; ++i) v[i] = (T)0.f;
+    if (left >= VEC) {
+        if constexpr (ANY)
+            v = *reinterpret_cast<const typename Vec<T, VEC>::any *>(p);
+        else
+            v = *reinterpret_cast<const typename Vec<T, VEC>::type *>(p);
+    } else if (ANY) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = i < left ? (float)p[i] : 0.f;
-        }
+        for (int i = 0; i < VEC; ++i)
+            if (i < left) v[i] = p[i];
     }
+    return v;
 }
 
 template <typename T, int VEC, bool ANY>
 __device__ __forceinline__ void store_row(T *p, int left, const float *v) {
     if constexpr (!ANY) {
-        store_vec<T, VEC>(p, v);
+        if (left >= VEC) store_vec<T, VEC>(p, v);
+    } else if (left >= VEC) {
+        typename Vec<T, VEC>::any r;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[i] = (T)v[i];
+        *reinterpret_cast<typename Vec<T, VEC>::any *>(p) = r;
     } else {
-        typedef T vt __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
-        if (left >= VEC) {
-            vt r;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) r[i] = (T)v[i];
-            *reinterpret_cast<vt *>(p) = r;
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (i < left) p[i] = (T)v[i];
-        }
+        for (int i = 0; i < VEC; ++i)
+            if (i < left) p[i] = (T)v[i];
     }
 }
 
-// VEC elements a load, NV loads a thread: n <= blockDim * NV * VEC. w is read
-// twice (from L2) rather than held: fewer registers, more rows in flight.
-template <typename TX, typename TY, int VEC, int NV, bool ANY>
-__global__ __launch_bounds__(1024) void rmsnorm_kernel(const NormArgs a) {
+// VEC elements a load, NV loads a thread: n <= blockDim * NV * VEC. LOOP: a
+// block takes every gridDim-th row, with w in registers and the next row's
+// loads in flight while it reduces and writes one.
+template <typename TX, typename TY, int VEC, int NV, bool ANY, bool LOOP>
+__global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormArgs a) {
     constexpr bool CODE = IsCode<TY>::value;
-    __shared__ float red[16];
-    __shared__ double red64[16];
-    const long row = blockIdx.x;
+    __shared__ float red[2][16]; // of odd and even rows: one barrier a row
+    __shared__ double red64[2][16];
     const int tid = threadIdx.x, nt = blockDim.x, n = a.n;
-    const TX *x = (const TX *)a.x + row * a.xs;
-    const TX *res = a.res ? (const TX *)a.res + row * a.rs : nullptr;
-    float v[NV][VEC];
+    typename Vec<TX, VEC>::type nx[NV], nr[NV];
+    auto fetch = [&](long row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = (j * nt + tid) * VEC;
+            nx[j] = load_row<TX, VEC, ANY>((const TX *)a.x + row * a.xs + e, n - e);
+            if (a.res) nr[j] = load_row<TX, VEC, ANY>((const TX *)a.res + row * a.rs + e, n - e);
+        }
+    };
+    fetch(blockIdx.x);
+    float w[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int e = (j * nt + tid) * VEC;
+        const auto x = load_row<float, VEC, ANY>(a.w + (j * nt + tid) * VEC, n - (j * nt + tid) * VEC);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
-        if (e < n) load_row<TX, VEC, ANY>(x + e, n - e, v[j]);
+        for (int i = 0; i < VEC; ++i) w[j][i] = x[i];
     }
-    if (res) {
-        float r[NV][VEC];
+    int buf = 0;
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        float v[NV][VEC];
+        // w is the same in every round, but its fp64 forms are not to be kept: they would take twice its registers
+        if (CODE && LOOP) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = (j * nt + tid) * VEC;
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) r[j][i] = 0.f;
-            if (e < n) load_row<TX, VEC, ANY>(res + e, n - e, r[j]);
+                for (int i = 0; i < VEC; ++i) asm volatile("" : "+v"(w[j][i]));
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j][i] += r[j][i];
-    }
-    float sq = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sq = fmaf(v[j][i], v[j][i], sq);
-    double top = 0.0; // max |r * w|, in fp64, where the products are exact
-    if constexpr (CODE) {
-        // rounding to fp32 keeps the order, so a thread's largest is among its products at its fp32 maximum
-        float t = 0.f, w[NV][VEC];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = (j * nt + tid) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w[j][i] = 0.f;
-            if (e < n) load_row<float, VEC, ANY>(a.w + e, n - e, w[j]);
-        }
+            for (int i = 0; i < VEC; ++i) v[j][i] = a.res ? (float)nx[j][i] + (float)nr[j][i] : (float)nx[j][i];
+        if (LOOP && row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        float sq = 0.f, t = 0.f;
+        double top = 0.0; // max |r * w|, in fp64, where the products are exact
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) t = fmaxf(t, fabsf(v[j][i] * w[j][i]));
+            for (int i = 0; i < VEC; ++i) {
+                sq = fmaf(v[j][i], v[j][i], sq);
+                if (CODE) t = fmaxf(t, fabsf(v[j][i] * w[j][i]));
+            }
+        if constexpr (CODE) {
+            // rounding to fp32 keeps the order, so a thread's largest is among its products at its fp32 maximum
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (fabsf(v[j][i] * w[j][i]) == t) top = fmax(top, fabs((double)v[j][i] * (double)w[j][i]));
-    }
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-        sq += __shfl_xor(sq, m);
-        if (CODE) top = max_across(top, m);
-    }
-    if (nt > 64) {
-        if ((tid & 63) == 0) {
-            red[tid >> 6] = sq;
-            if (CODE) red64[tid >> 6] = top;
+                for (int i = 0; i < VEC; ++i)
+                    if (fabsf(v[j][i] * w[j][i]) == t) top = fmax(top, fabs((double)v[j][i] * (double)w[j][i]));
         }
-        __syncthreads();
-        sq = 0.f;
-        for (int i = 0; i < nt >> 6; ++i) {
-            sq += red[i];
-            if (CODE) top = fmax(top, red64[i]);
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) {
+            sq += __shfl_xor(sq, m);
+            if (CODE) top = fmax(top, __shfl_xor(top, m));
         }
-    }
-    const float rstd = 1.0f / sqrtf(sq / (float)n + a.eps);
-    if (a.sum) {
-        TX *s = (TX *)a.sum + row * a.ss;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = (j * nt + tid) * VEC;
-            if (e < n) store_row<TX, VEC, ANY>(s + e, n - e, v[j]);
-        }
-    }
-    TY *y = (TY *)a.y + row * a.ys;
-    if constexpr (!CODE) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = (j * nt + tid) * VEC;
-            if (e < n) {
-                float o[VEC], w[VEC];
-                load_row<float, VEC, ANY>(a.w + e, n - e, w);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[i];
-                store_row<TY, VEC, ANY>(y + e, n - e, o);
+        if (nt > 64) {
+            if ((tid & 63) == 0) {
+                red[buf][tid >> 6] = sq;
+                if (CODE) red64[buf][tid >> 6] = top;
+            }
+            __syncthreads();
+            sq = 0.f;
+            for (int i = 0; i < nt >> 6; ++i) {
+                sq += red[buf][i];
+                if (CODE) top = fmax(top, red64[buf][i]);
             }
         }
-    } else {
-        const float scale = (float)(top * (double)rstd / 127.0);
-        if (tid == 0) a.y_scale[row] = scale;
-        // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
-        const bool ok = top > 0.0 && scale == scale;
-        const float inv = 127.0f / (float)top;
-        const bool range = top > 1e-30 && top < 1e30; // fp32 holds the products and inv
+        const float rstd = 1.0f / sqrtf(sq / (float)n + a.eps);
+        if (a.sum) {
+            TX *s = (TX *)a.sum + row * a.ss;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = (j * nt + tid) * VEC;
-            if (e < n) {
-                float o[VEC], w[VEC];
-                load_row<float, VEC, ANY>(a.w + e, n - e, w);
+            for (int j = 0; j < NV; ++j) {
+                const int e = (j * nt + tid) * VEC;
+                store_row<TX, VEC, ANY>(s + e, n - e, v[j]);
+            }
+        }
+        TY *y = (TY *)a.y + row * a.ys;
+        if constexpr (!CODE) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = (j * nt + tid) * VEC;
+                float o[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[j][i];
+                store_row<TY, VEC, ANY>(y + e, n - e, o);
+            }
+        } else {
+            const float scale = (float)(top * (double)rstd / 127.0);
+            if (tid == 0) a.y_scale[row] = scale;
+            // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
+            const bool ok = top > 0.0 && scale == scale;
+            const bool range = top > 1e-30 && top < 1e30; // fp32 holds the products and the quotient's factor
+            const double inv64 = 127.0 / top;
+            const float inv = (float)inv64;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = (j * nt + tid) * VEC;
+                float o[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float f = v[j][i] * w[i] * inv; // within 127 * 4 * 2^-24 of the quotient
+                    // within 127 * 4 * 2^-24 of the quotient
+                    const float f = range ? v[j][i] * w[j][i] * inv : (float)((double)v[j][i] * (double)w[j][i] * inv64);
                     float c = rintf(f);
-                    if (!range || fabsf(f - c) > 0.4999f) // next to a border: decide in fp64
-                        c = (float)rint((double)v[j][i] * (double)w[i] * 127.0 / top);
+                    if (fabsf(f - c) > 0.4999f) { // next to a border: on which side, in fp64 and without a division
+                        const float k = floorf(f);
+                        const double d = fma(-(double)(k + 0.5f), top, (double)v[j][i] * (double)w[j][i] * 127.0);
+                        c = d > 0.0 ? k + 1.f : d < 0.0 ? k : 2.f * rintf(0.5f * (k + 0.5f)); // a tie: the even one
+                    }
                     o[i] = ok ? c : 0.f;
                 }
                 store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         }
+        if (!LOOP) break;
     }
 }
 
@@ -203,11 +204,19 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     }
     int nt = ((chunks + nv - 1) / nv + 63) / 64 * 64;
     if (nt > 1024) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)a.rows), block((unsigned)nt);
+    // 16 waves a CU then hold a row each and the next one's loads
+    const long most = (long)cus * (1024 / nt);
+    const bool loop = nt <= 512 && a.rows > most;
+    const dim3 grid((unsigned)(loop ? most : a.rows)), block((unsigned)nt);
     switch (nv) {
-#define WQ_NV(N)                                                                                         \
-    case N:                                                                                              \
-        if constexpr (N <= LAST) hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY>), grid, block, 0, st, a); \
+#define WQ_NV(N)                                                                                                       \
+    case N:                                                                                                            \
+        if constexpr (N <= LAST) {                                                                                     \
+            if (loop)                                                                                                  \
+                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, true>), grid, block, 0, st, a);                \
+            else                                                                                                       \
+                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, false>), grid, block, 0, st, a);               \
+        }                                                                                                              \
         break;
         WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8)
 #undef WQ_NV
