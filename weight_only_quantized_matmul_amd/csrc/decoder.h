@@ -122,18 +122,6 @@ __device__ __forceinline__ void store_vec(T *p, const float *v) {
     *reinterpret_cast<vt *>(p) = r;
 }
 
-// The sequence that holds token `tok`: the number of q_start[1..B] that are
-// <= tok, counted by a group of LANES lanes (a power of two) that all call
-// with the same token. q_start is ascending.
-template <int LANES>
-__device__ __forceinline__ int sequence_of(const int *q_start, int B, int tok, int lane) {
-    int n = 0;
-    for (int i = 1 + lane; i <= B; i += LANES) n += q_start[i] <= tok ? 1 : 0;
-#pragma unroll
-    for (int m = LANES / 2; m > 0; m >>= 1) n += __shfl_xor(n, m);
-    return n;
-}
-
 // Position / page, for positions below 2^31.
 __device__ __forceinline__ int page_index(const KvView &c, int t) {
     return c.page_mul ? (int)(__umulhi((uint32_t)t, c.page_mul) >> c.page_shift) : t;

@@ -47,7 +47,7 @@ struct Where {
 };
 
 template <int LANES, int RPG>
-__device__ __forceinline__ Where locate(const KvCopyArgs &a, int lane) {
+__device__ __forceinline__ Where token_of(const KvCopyArgs &a) {
     Where w;
     const unsigned parts = (2 * a.c.heads + RPG - 1) / RPG;
     const unsigned r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
@@ -55,20 +55,34 @@ __device__ __forceinline__ Where locate(const KvCopyArgs &a, int lane) {
     w.any = tok < (unsigned)a.b.T;
     w.tok = w.any ? (int)tok : 0;
     w.first = (int)(r - tok * parts) * RPG;
-    const int b = sequence_of<LANES>(a.b.q_start, a.b.B, w.tok, lane);
-    w.there = false;
-    w.row = w.scale = 0;
-    if (w.any && b < a.b.B) {
-        const int first = a.b.q_start[b], next = a.b.q_start[b + 1];
-        const long t = (long)a.b.kv_len[b] - next + w.tok;
-        int page, slot;
-        if (first <= w.tok && w.tok < next && find_row(a.c, a.b, b, t, &page, &slot)) {
-            w.there = true;
-            w.row = page * a.c.rp + slot * a.c.rs;
-            w.scale = page * a.c.sp + slot * a.c.ss;
+    return w;
+}
+
+// Where the token lies. The lanes of a group read starts and lengths together (one round trip), then the one
+// whose sequence holds the token tells the others; the page's entry is the only load that waits for them.
+template <int LANES>
+__device__ __forceinline__ void locate(const KvCopyArgs &a, Where &w, int lane) {
+    int seq = -1, t = -1;
+    for (int i = lane; i < a.b.B; i += LANES) {
+        const int first = a.b.q_start[i], next = a.b.q_start[i + 1], kv = a.b.kv_len[i];
+        if (first <= w.tok && w.tok < next) {
+            seq = i;
+            t = kv - next + w.tok;
         }
     }
-    return w;
+    const int base = (threadIdx.x & 63) - lane;
+    const uint64_t hits = __ballot(seq >= 0) >> base & (LANES == 64 ? ~0ull : (1ull << LANES) - 1);
+    const int from = base + (hits ? __builtin_ctzll(hits) : 0);
+    seq = __shfl(seq, from);
+    t = __shfl(t, from);
+    w.there = false;
+    w.row = w.scale = 0;
+    int page, slot;
+    if (w.any && hits && find_row(a.c, a.b, seq, t, &page, &slot)) {
+        w.there = true;
+        w.row = page * a.c.rp + slot * a.c.rs;
+        w.scale = page * a.c.sp + slot * a.c.ss;
+    }
 }
 
 // The largest over a group of LANES lanes.
@@ -83,16 +97,17 @@ template <typename T, int KIND, int D, bool VEC, int RPG>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvCopyArgs a) {
     constexpr int LANES = D / 8;
     const int lane = threadIdx.x & (LANES - 1), H = a.c.heads;
-    const Where w = locate<LANES, RPG>(a, lane);
+    Where w = token_of<LANES, RPG>(a);
     float v[RPG][8];
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const int s = w.first + j, side = s >= H;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-        if (w.there && s < 2 * H)
+        if (w.any && s < 2 * H)
             load8<T, VEC>((const T *)(side ? a.v : a.k) + (long)w.tok * a.tok + (long)(s - side * H) * a.head + 8 * lane, v[j]);
     }
+    locate<LANES>(a, w, lane);
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const int s = w.first + j, side = s >= H, head = s - side * H;
@@ -149,7 +164,8 @@ template <typename T, int KIND, int D, bool VEC, int RPG>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(const KvCopyArgs a) {
     constexpr int LANES = D / 8, W = Codes<KIND>::bytes / 4;
     const int lane = threadIdx.x & (LANES - 1), H = a.c.heads;
-    const Where w = locate<LANES, RPG>(a, lane);
+    Where w = token_of<LANES, RPG>(a);
+    locate<LANES>(a, w, lane);
     if (!w.any) return;
     typedef uint32_t words __attribute__((ext_vector_type(W)));
     words u[RPG];
