@@ -470,10 +470,11 @@ int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_o
  * unseen positions hold (infinities and NaN among it) never enters a result.
  * q, o: [T, H, dim] of dtype (f32, bf16, f16) with strides; H a multiple of
  * the cache's heads; lse: float [T, H], contiguous, or NULL. The softmax
- * statistics and all sums are fp32. f32 queries and probabilities enter the
- * matrix units as two f16 parts (22 bits and more), bf16/f16 queries exactly,
- * their probabilities rounded to f16 (2^-12, below the output's rounding); the
- * codes are exact.
+ * statistics and all sums are fp32; codes enter the matrix units exactly.
+ * f32 queries enter as two f16 parts (22 bits and more), their probabilities
+ * as three bf16 parts (24 bits) against integer codes and as two f16 parts
+ * against f16 codes (22 bits, down to 2^-39 of a row's largest); bf16/f16
+ * queries enter exactly, their probabilities rounded to f16 (2^-11).
  * Where the positions are split among blocks, partial results pass through
  * the stream's workspace as in wq_matmul_dev (it may grow; while the stream
  * is being captured it cannot: warm up first, else WQ_E_UNSUPPORTED).

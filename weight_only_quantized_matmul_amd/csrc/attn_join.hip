@@ -1,33 +1,35 @@
 // Attention rows whose positions were split among blocks: the partial results
 // become one.
 //
-// Bound by latency, so nothing waits for what it does not need: a block of four
-// waves takes one row, each wave every fourth split, and the first partial rows
-// are read before it is known how many there are (their places depend on the
+// Bound by latency, so nothing waits for what it does not need: four waves take
+// a row, each every fourth split (one wave where there are rows for every CU
+// and few splits), and the first partial rows are read before it is known how many there are (their places depend on the
 // row alone) beside the lengths from which that follows. With the lengths read
-// one after another and one wave a row the join of 32 splits took 17 us.
+// one after another and one wave a row the join of 32 splits took 17 us, now 5 us.
 #include "attn_common.h"
 
 namespace wq {
 namespace {
 
-// kAtOnce: partial rows a wave has in flight
-template <typename T, int D, int kAtOnce>
+// AT: partial rows a wave has in flight; WPR: waves a row (1 or 4)
+template <typename T, int D, int AT, int WPR>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, const Partials pt, const int R, const int step) {
     constexpr int E = D / 64; // elements a lane
     __shared__ float sh_o[3][D], sh_l[3];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const long row = blockIdx.x;
+    const int lane = threadIdx.x & 63, at_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = WPR == 1 ? 0 : at_wave;
+    const long row = WPR == 1 ? (long)blockIdx.x * 4 + at_wave : blockIdx.x;
+    if (row >= (long)a.b.T * a.H) return;
     const int G = a.H / a.c.heads;
     const int tok = (int)(row / a.H), h = (int)(row % a.H);
     const float *ml = pt.ml + row * pt.nsplit * 2, *part = pt.part + row * pt.nsplit * D + lane * E;
-    // splits lane, lane + 64, ... for the references; splits wave, wave + 4, ... for the rows
+    // splits lane, lane + 64, ... for the references; splits wave, wave + WPR, ... for the rows
     float ref = lane < pt.nsplit ? ml[2 * lane] : -INFINITY;
-    float v[kAtOnce][E], r[kAtOnce], l[kAtOnce];
+    float v[AT][E], r[AT], l[AT];
     auto read = [&](int s0) {
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int s = min(s0 + 4 * k, pt.nsplit - 1);
+        for (int k = 0; k < AT; ++k) {
+            const int s = min(s0 + WPR * k, pt.nsplit - 1);
             load_vec<float, E>(part + (long)s * D, v[k]);
             r[k] = ml[2 * s];
             l[k] = ml[2 * s + 1];
@@ -73,29 +75,31 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, const 
     for (int k = 32; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor(M, k));
     const float base = M == -INFINITY ? 0.f : M;
     float L = 0.f, o[E] = {};
-    for (int first = wave; first < sp.splits; first += 4 * kAtOnce) {
+    for (int first = wave; first < sp.splits; first += WPR * AT) {
         if (first != wave) read(first);
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const bool on = first + 4 * k < sp.splits; // what stands past the splits is not looked at
+        for (int k = 0; k < AT; ++k) {
+            const bool on = first + WPR * k < sp.splits; // what stands past the splits is not looked at
             const float f = on ? __builtin_amdgcn_exp2f(r[k] - base) : 0.f;
             L = on ? fmaf(l[k], f, L) : L;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = on ? fmaf(v[k][e], f, o[e]) : o[e];
         }
     }
-    if (wave > 0) {
+    if constexpr (WPR > 1) {
+        if (wave > 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sh_o[wave - 1][lane * E + e] = o[e];
-        if (lane == 0) sh_l[wave - 1] = L;
-    }
-    __syncthreads();
-    if (wave > 0) return;
+            for (int e = 0; e < E; ++e) sh_o[wave - 1][lane * E + e] = o[e];
+            if (lane == 0) sh_l[wave - 1] = L;
+        }
+        __syncthreads();
+        if (wave > 0) return;
 #pragma unroll
-    for (int w = 0; w < 3; ++w) {
-        L += sh_l[w];
+        for (int w = 0; w < 3; ++w) {
+            L += sh_l[w];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += sh_o[w][lane * E + e];
+            for (int e = 0; e < E; ++e) o[e] += sh_o[w][lane * E + e];
+        }
     }
     const bool none = M == -INFINITY && L == 0.f;
     const float inv = none ? 0.f : 1.0f / L;
@@ -109,14 +113,14 @@ template <typename T, int D>
 hipError_t launch_d(const AttnArgs &a, const AttnPlan &p, const Partials &pt, hipStream_t st) {
     const long rows = (long)a.b.T * a.H;
     if (rows > 0x7fffffffL) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)rows), block(256);
-    // as many as four waves need for all splits, at most eight
-    if (pt.nsplit <= 4)
-        hipLaunchKernelGGL((attn_join_kernel<T, D, 1>), grid, block, 0, st, a, pt, p.rows, p.step);
+    const dim3 block(256);
+    // enough partial rows in flight for all splits, at most eight a wave
+    if (rows >= 1024 && pt.nsplit <= 16)
+        hipLaunchKernelGGL((attn_join_kernel<T, D, 4, 1>), dim3((unsigned)((rows + 3) / 4)), block, 0, st, a, pt, p.rows, p.step);
     else if (pt.nsplit <= 8)
-        hipLaunchKernelGGL((attn_join_kernel<T, D, 2>), grid, block, 0, st, a, pt, p.rows, p.step);
+        hipLaunchKernelGGL((attn_join_kernel<T, D, 2, 4>), dim3((unsigned)rows), block, 0, st, a, pt, p.rows, p.step);
     else
-        hipLaunchKernelGGL((attn_join_kernel<T, D, 8>), grid, block, 0, st, a, pt, p.rows, p.step);
+        hipLaunchKernelGGL((attn_join_kernel<T, D, 8, 4>), dim3((unsigned)rows), block, 0, st, a, pt, p.rows, p.step);
     return hipGetLastError();
 }
 

