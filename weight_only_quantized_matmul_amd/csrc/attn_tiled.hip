@@ -3,9 +3,9 @@
 //
 // A block of NW waves takes a tile of RW * NW rows and walks the positions in
 // steps of TK. K goes to LDS as f16 rows, V transposed, so both are read back
-// as whole 16-byte operands; the next steps' codes are in flight from HBM or L2
-// meanwhile, and three buffers of K and two of V leave one barrier a step. Per
-// step a wave computes for its RW rows
+// as whole 16-byte operands; the next step's codes are in flight from HBM or L2
+// meanwhile, and two buffers leave one barrier a step. Per step a wave computes
+// for its RW rows
 //     S^T[key][row]  = sum_d K[key][d] Q[row][d]           (A = K, B = Q)
 //     O^T[d][row]   += sum_key V^T[d][key] P^T[key][row]   (A = V^T, B = P^T)
 // with v_mfma_f32_32x32x16 (RW = 32) or 16x16x32 (RW = 16: rows of 256
@@ -48,7 +48,7 @@ struct Mma<16> {
 template <typename T, int KIND, int D, int NW>
 struct Tiled {
     static constexpr int RW = tiled_rows(D, sizeof(T) == 4); // rows a wave
-    static constexpr int TK = D == 256 ? 32 : 64;    // positions a step (LDS: 5 buffers of TK * D halves)
+    static constexpr int TK = D == 256 ? 32 : 64;    // positions a step (LDS: 4 buffers of TK * D halves, two blocks a CU)
     static constexpr int NT = 64 * NW, R = RW * NW;
     static constexpr int NG = 64 / RW;               // lanes that share a row
     static constexpr int CH = D / 8, CV = TK / 8;    // 16-byte chunks of a K row and of a V^T row in LDS
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     typedef Tiled<T, KIND, D, NW> F;
     constexpr int RW = F::RW, NG = F::NG, TK = F::TK, P = F::P;
     typedef typename Mma<RW>::acc acc;
-    __shared__ __align__(16) uint8_t sk[3 * F::KSIZE];
+    __shared__ __align__(16) uint8_t sk[2 * F::KSIZE];
     __shared__ __align__(16) uint8_t sv[2 * F::VSIZE];
     __shared__ OFF s_off[4][TK], s_sc[4][TK]; // rows (bytes) and scales (floats) of a step's positions
     __shared__ float s_ks[2][TK], s_vs[2][TK], s_big[2];
@@ -341,10 +341,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     constexpr int KAHEAD = KWANT < KN ? KWANT : KN, VAHEAD = VWANT < VN ? VWANT : VN;
     const int k_lane = n * F::KROW + g * 16, v_lane = n % F::VE * F::VGROUP + n / F::VE * F::VROW + g * 16;
     acc s[F::KBH];
-    auto scores = [&](int k3, int h, auto beside) { // S^T of part h from K buffer k3; beside(0 .. NQH - 1) as reads end
+    auto scores = [&](int kbuf, int h, auto beside) { // S^T of part h from K buffer kbuf; beside(0 .. NQH - 1) as reads end
         constexpr int N = KN;
         f16x8 fr[KAHEAD];
-        const uint8_t *from = sk + k3 * F::KSIZE + h * F::KBH * RW * F::KROW + k_lane;
+        const uint8_t *from = sk + kbuf * F::KSIZE + h * F::KBH * RW * F::KROW + k_lane;
         auto read = [&](int x) { return *reinterpret_cast<const f16x8 *>(from + x % F::KBH * RW * F::KROW + x / F::KBH * NG * 16); };
 #pragma unroll
         for (int x = 0; x < KAHEAD; ++x) fr[x] = read(x);
@@ -371,13 +371,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     // does the wave work on step i?
     auto active = [&](int i) { return working && i < blk1 && sp.base + i * TK < w_hi && sp.base + i * TK + TK > w_lo; };
 
-    // Step t of this split works on block blk0 + t. Before barrier 0: K of steps 0 and 1, V and scales of step 0,
-    // offsets of steps 0 to 2.
+    // Step c of this split works on block blk0 + c. Before its barrier: its K, V and scales, places of it and the next.
     if (wave == 0) {
-        const Key k0 = look(blk0), k1 = look(blk0 + 1), k2 = look(blk0 + 2);
+        const Key k0 = look(blk0), k1 = look(blk0 + 1);
         put_place(0, place(k0));
         put_place(1, place(k1));
-        put_place(2, place(k2));
         if (lane == 0) s_bad[0] = s_bad[1] = s_bad[2] = 0;
     }
     __syncthreads();
@@ -386,23 +384,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
         fetch_k(s_off[0]);
         fetch_v(s_off[0]);
         store_k(0);
-        fetch_k(s_off[1]);
         store_v(0, 0, s_mask[0], is_edge(blk0, s_mask[0]));
-        store_k(1);
     }
     __syncthreads();
 
-    for (int i = blk0, k3 = 0; i < blk1; ++i) {
+    for (int i = blk0; i < blk1; ++i) {
         const int c = i - blk0, buf = c & 1, t0 = sp.base + i * TK;
-        const int k3n = k3 == 2 ? 0 : k3 + 1, k3nn = k3n == 2 ? 0 : k3n + 1; // K buffers of steps t + 1, t + 2
         const uint64_t mask = s_mask[c & 3], mask_next = s_mask[(c + 1) & 3];
         const float big_all = F::BF ? 0.f : s_big[buf];
         const int bad_now = KIND == WQ_KV_F16 ? s_bad[c % 3] : 0;
-        fetch_k(s_off[(c + 2) & 3]); // past the last step: row 0 again, unused
+        fetch_k(s_off[(c + 1) & 3]); // past the last step: row 0 again, unused
         fetch_v(s_off[(c + 1) & 3]);
-        Key key3;
+        Key key2;
         float scale1 = 0.f;
-        if (wave == 0) key3 = look(i + 3);
+        if (wave == 0) key2 = look(i + 2);
         if (wave == 1 || wave == 2) scale1 = get_scale((c + 1) & 3);
         if (active(i)) {
 #pragma unroll
@@ -410,7 +405,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
             f32x4 ksq[F::NQH], vsq[F::NQH]; // scales of keys and values, read ahead of their use
             const float *ks_at = &s_ks[buf][h * (TK / F::HV) + 4 * g], *vs_at = &s_vs[buf][h * (TK / F::HV) + 4 * g];
             __builtin_amdgcn_s_setprio(1);
-            scores(k3, h, [&](int j) { ksq[j] = *reinterpret_cast<const f32x4 *>(ks_at + 4 * NG * j); });
+            scores(buf, h, [&](int j) { ksq[j] = *reinterpret_cast<const f32x4 *>(ks_at + 4 * NG * j); });
             __builtin_amdgcn_s_setprio(0);
 #pragma unroll
             for (int j = 0; j < F::NQH; ++j)
@@ -541,11 +536,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
         }
         }
         if (KIND == WQ_KV_F16 && tid == 0) s_bad[(c + 2) % 3] = 0;
-        store_k(k3nn);
+        store_k(buf ^ 1);
         store_v(buf ^ 1, c + 1, mask_next, is_edge(i + 1, mask_next));
-        if (wave == 0) put_place((c + 3) & 3, place(key3));
+        if (wave == 0) put_place((c + 2) & 3, place(key2));
         if (wave == 1 || wave == 2) put_scale(buf ^ 1, (c + 1) & 3, scale1);
-        k3 = k3n;
         __syncthreads();
     }
 

@@ -124,15 +124,20 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     if (b->max_kv > 0 && b->max_kv < kv) kv = b->max_kv;
     if (window > 0 && causal && (long)window + q < kv) kv = (long)window + q;
     const int row = c->kind == WQ_KV_F16 ? 2 * c->dim : c->kind == WQ_KV_I8 ? c->dim : c->dim / 2;
-    p.few = q * G <= (c->dim <= 128 ? 32 : 16);
+    // Up to 64 rows (32 of 256 elements) the few-rows kernel reads the cache once a tile of 32 (16) rows, the second
+    // time from L2, and still beats tiles of which half the rows are empty (60 rows on 19531 positions: 38 us, tiled 70;
+    // on 38 positions 14.6 and 13.6).
+    p.few = q * G <= (c->dim <= 128 ? 64 : 32);
     p.waves = 4;
     if (p.few) {
-        p.rows = q * G > 16 ? 32 : 16;
+        p.rows = q * G > 16 && c->dim <= 128 ? 32 : 16;
         p.step = row <= 128 ? 64 : 32;
     } else {
-        // eight waves share each opened tile when their larger tiles still give every CU a block
+        // Eight waves share each opened tile where opening is dear (rows of 128 and 256) and their larger tiles still
+        // give every CU a block: prefill of 4096 tokens 216 us, with four waves 268. Rows of 64 do better with more,
+        // smaller blocks (13 prompts of up to 1695 tokens, window 507: four waves 43 us, eight 91).
         const long wave_rows = wq::tiled_rows(c->dim, f32);
-        if ((q * G + 8 * wave_rows - 1) / (8 * wave_rows) * b->B * c->heads >= cus) p.waves = 8;
+        if (c->dim > 64 && (q * G + 8 * wave_rows - 1) / (8 * wave_rows) * b->B * c->heads >= cus) p.waves = 8;
         p.rows = (int)wave_rows * p.waves;
         p.step = c->dim == 256 ? 32 : 64;
     }
