@@ -18,7 +18,7 @@
 // instructions and an exponential an element). 4096 tokens, causal, 32 heads over
 // 8, bf16 on an f16 cache: 137 GFLOP in 200 us (686 TFLOP/s); eight chunks of up
 // to 511 tokens on up to 5000 positions, f32 on int8: 159 GFLOP, 2.5 times that
-// in parts, in 454 us.
+// in parts, in 456 us.
 #include "attn_common.h"
 
 namespace wq {

@@ -99,7 +99,7 @@ int kv_copy(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k, void *v
     const int size = size_of(dtype);
     if (k == nullptr || v == nullptr || !aligned(k, size) || !aligned(v, size)) return WQ_E_INVAL;
     if ((rc = wq::begin_call(cache->device)) != WQ_OK) return rc;
-    if ((long)batch->T * 2 * cache->heads > (long)INT_MAX * 8) return WQ_E_UNSUPPORTED;
+    if ((long)batch->T * 2 * cache->heads > (long)INT_MAX) return WQ_E_UNSUPPORTED;
     DeviceScope scope(cache->device);
     wq::KvCopyArgs a;
     a.c = view(cache);
