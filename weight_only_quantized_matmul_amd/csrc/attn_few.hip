@@ -38,7 +38,7 @@ struct Few {
     static constexpr int P = sizeof(T) == 4 ? 2 : 1;                                    // f16 parts of q
     static constexpr bool BF = P == 2 && KIND != WQ_KV_F16;                             // p and v in bf16
     static constexpr int PP = BF ? 3 : P;                                               // parts of p
-    static constexpr int TK = RB <= 128 ? 64 : 32;                                      // positions a block
+    static constexpr int TK = RB <= 64 ? 64 : 32;                                      // positions a block
     static constexpr int LB = RB / 4 < 16 ? RB / 4 : 16; // bytes of one K load
     static constexpr int KL = RB / 4 / LB;               // K loads a lane and key
     static constexpr int KW = LB / 4;                    // words of one

@@ -131,7 +131,7 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     p.waves = 4;
     if (p.few) {
         p.rows = q * G > 16 && c->dim <= 128 ? 32 : 16;
-        p.step = row <= 128 ? 64 : 32;
+        p.step = row <= 64 ? 64 : 32;
     } else {
         // Eight waves share each opened tile where opening is dear (rows of 128 and 256) and their larger tiles still
         // give every CU a block: prefill of 4096 tokens 216 us, with four waves 268. Rows of 64 do better with more,
@@ -147,9 +147,9 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     const long total = (tiles < numbers ? tiles : numbers) * c->heads * steps;
     if (p.few) {
         long per_wave = total / (cus * 12);
-        // many sequences differ in length: shorter splits even that out (64 ragged sequences: 150 us with 8 steps a wave,
-        // 155 with 16); few are split for the chip's sake and pay for each split's start (4 long ones: 179 and 154 us)
-        const long most = (tiles < numbers ? tiles : numbers) * c->heads >= cus ? 8 : 16;
+        // many sequences differ in length: shorter splits even that out (64 ragged sequences: 150 us with 512 positions
+        // a wave, 155 with 1024); few are split for the chip's sake and pay for each split's start (4 long ones: 179 and 154 us)
+        const long most = ((tiles < numbers ? tiles : numbers) * c->heads >= cus ? 512 : 1024) / p.step;
         per_wave = per_wave < 1 ? 1 : per_wave > most ? most : per_wave;
         p.least = (int)(4 * per_wave);
     } else {
