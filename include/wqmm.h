@@ -188,10 +188,14 @@ int wq_matmul_t(const wq_tensor *t, const float *x, int S, float *y);
  * stream that gets the same handle, so let a stream's queued calls finish
  * before destroying it. A call being captured into a HIP graph never waits
  * or allocates: it uses its stream's workspace if that is large enough,
- * else the largest workspace on the device that is (the graph then shares
- * that stream's buffer: do not replay it while that stream runs tiled
- * calls), else it returns WQ_E_UNSUPPORTED; so run the largest S once,
- * eagerly, before capturing.
+ * else the largest workspace on the device that is, else it returns
+ * WQ_E_UNSUPPORTED; so run the largest S once, eagerly, before capturing.
+ * A graph keeps the buffer that its calls were captured with: that buffer
+ * is never freed and never passes to another stream, whatever calls follow
+ * (a stream that needs more gets a new one and leaves the old one, until
+ * the process ends, to the graph). The stream it was captured from goes on
+ * with the buffer until then, so do not replay the graph while that stream,
+ * or another graph with the same buffer, runs calls that use a workspace.
  */
 int wq_matmul_dev(const wq_tensor *t, const float *x_dev, int S, float *y_dev, void *hip_stream);
 
@@ -477,7 +481,8 @@ int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_o
  * queries enter exactly, their probabilities rounded to f16 (2^-11).
  * Where the positions are split among blocks, partial results pass through
  * the stream's workspace as in wq_matmul_dev (it may grow; while the stream
- * is being captured it cannot: warm up first, else WQ_E_UNSUPPORTED).
+ * is being captured it cannot: warm up first, else WQ_E_UNSUPPORTED; a graph
+ * keeps the buffer it was captured with, also after the stream's has grown).
  */
 int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *q, int dtype, int H, long q_tok,
                       long q_head, float scale, int causal, int window, void *o, long o_tok, long o_head, float *lse,

@@ -18,6 +18,7 @@
 #include <new>
 
 #include "decoder.h"
+#include "stream_workspaces.h"
 #include "skinny_group.h"
 #include "staging.h"
 #include "wq_internal.h"
@@ -52,20 +53,11 @@ struct DeviceCtx {
     size_t hx_cap = 0;  // bytes
     float *h_y = nullptr, *dh_y = nullptr;
     size_t hy_cap = 0;  // bytes
-    // Tiled workspaces (activation planes, split-K partials, the gated
-    // intermediate), one per stream that ran such a call, so calls on
-    // different streams may overlap. At most kStreamWorkspaces per device;
-    // a new stream beyond that takes over the least recently used one.
-    struct StreamWs {
-        hipStream_t st = nullptr;
-        bool live = false;
-        uint16_t *p = nullptr;
-        size_t cap = 0;  // bytes
-        unsigned long long last = 0;
-    };
-    static constexpr int kStreamWorkspaces = 8;
-    StreamWs ws[kStreamWorkspaces];
-    unsigned long long ws_clock = 0;
+    // Workspaces (activation planes, split-K partials, the gated
+    // intermediate, attention's partial results), one per stream that ran
+    // such a call, so calls on different streams may overlap. At most kSlots
+    // per device; a new stream beyond that takes over the least recently used.
+    wq::StreamWorkspaces ws;
     size_t lib_bytes = 0;      // device bytes held by tensors, groups and the workspace
     std::recursive_mutex mu;
 };
@@ -213,14 +205,8 @@ int choose_path(int fmt, int O, int I, int S, int cus, wq::GemvPlan *gp, int gs 
     return 2;
 }
 
-// The workspace of stream `st`, grown to at least `bytes`. Only calls on
-// `st` use it, and they run in stream order, so it is reused without any
-// wait. Growing it, or handing a new stream the slot of the least recently
-// used one (every slot taken), waits for the device to go idle (the old
-// buffer may still be read). A call being captured into a graph never
-// waits or allocates: it takes its stream's workspace if that is large
-// enough, else the largest one that is (the graph then shares that
-// stream's buffer), else it is refused.
+// The workspace of stream `st`, grown to at least `bytes` (the rules stand in
+// stream_workspaces.h).
 int ensure_workspace(DeviceCtx &d, size_t bytes, hipStream_t st, uint16_t **out) {
     std::lock_guard<std::recursive_mutex> lk(d.mu);
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -228,53 +214,20 @@ int ensure_workspace(DeviceCtx &d, size_t bytes, hipStream_t st, uint16_t **out)
         (void)hipGetLastError();
         return WQ_E_HIP;
     }
-    DeviceCtx::StreamWs *e = nullptr;
-    for (DeviceCtx::StreamWs &c : d.ws)
-        if (c.live && c.st == st) e = &c;
-    if (cs != hipStreamCaptureStatusNone) {
-        if (e == nullptr || e->cap < bytes) {
-            e = nullptr;
-            for (DeviceCtx::StreamWs &c : d.ws)
-                if (c.live && c.cap >= bytes && (e == nullptr || c.cap > e->cap)) e = &c;
-        }
-        if (e == nullptr) return WQ_E_UNSUPPORTED;
-        *out = e->p;
-        return WQ_OK;
-    }
-    const bool adopt = e == nullptr;
-    if (adopt) {
-        for (DeviceCtx::StreamWs &c : d.ws)
-            if (!c.live && e == nullptr) e = &c;
-        if (e == nullptr) {
-            e = &d.ws[0];
-            for (DeviceCtx::StreamWs &c : d.ws)
-                if (c.last < e->last) e = &c;
-        }
-    }
-    // a taken-over slot may still be read by its previous stream's calls
-    if (bytes > e->cap || (adopt && e->live)) {
-        if (hipDeviceSynchronize() != hipSuccess) {
+    struct Memory {
+        DeviceCtx &d;
+        int alloc(void **p, size_t n) { return dev_alloc(d, p, n); }
+        void release(void *p, size_t n) { dev_free(d, p, n); }
+        int idle() {
+            if (hipDeviceSynchronize() == hipSuccess) return WQ_OK;
             (void)hipGetLastError();
             return WQ_E_HIP;
         }
-    }
-    if (bytes > e->cap) {
-        dev_free(d, e->p, e->cap);
-        e->p = nullptr;
-        e->cap = 0;
-        const size_t cap = (size_t)wq::round_up((long)bytes, 2L << 20);
-        int rc = dev_alloc(d, (void **)&e->p, cap);
-        if (rc != WQ_OK) {
-            e->live = false;
-            return rc;
-        }
-        e->cap = cap;
-    }
-    e->st = st;
-    e->live = true;
-    e->last = ++d.ws_clock;
-    *out = e->p;
-    return WQ_OK;
+    };
+    void *p = nullptr;
+    const int rc = d.ws.take(Memory{d}, bytes, st, cs != hipStreamCaptureStatusNone, WQ_E_UNSUPPORTED, &p);
+    if (rc == WQ_OK) *out = static_cast<uint16_t *>(p);
+    return rc;
 }
 
 // fixed_ws != nullptr: the workspace is that buffer of fixed_cap bytes (the
