@@ -356,7 +356,8 @@ int wq_stream_read_dev(const void *buf_dev, size_t bytes, int waves, int loads_i
  * the last dimension of every buffer is contiguous. Buffers must be aligned
  * to their element type; 16-byte aligned rows take the wide loads and others
  * a slower path with the same results. WQ_FAULT=launch makes each of them
- * return WQ_E_FAULT.
+ * return WQ_E_FAULT. Work that no launch holds (attention of more than about
+ * 16 million tiles, 2^31 cache rows a call) is refused with WQ_E_UNSUPPORTED.
  */
 enum wq_dtype { WQ_DT_F32 = 0, WQ_DT_BF16 = 1, WQ_DT_F16 = 2, WQ_DT_I8 = 3 };
 

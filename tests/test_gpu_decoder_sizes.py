@@ -1,0 +1,99 @@
+"""Calls with more work than one dimension of a launch holds (2^32 threads): they do all of it, or are refused.
+
+Inputs are windows of one buffer (a row starts a few elements after the last), so that the rows all differ and the
+memory stays small. Bounds are those of test_gpu_decoder.py: a norm's scale is within 38 u, codes and scales of the cache
+are exact."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import decoder_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - CPU hosts
+    pytest.skip("no GPU", allow_module_level=True)
+
+import gpu_util as gu  # noqa: E402
+import weight_only_quantized_matmul_amd as wq  # noqa: E402
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def device():
+    gu.reinit_with_env(WQ_FAULT=None, WQ_MEM_LIMIT_BYTES=None)
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_rope_of_many_tokens():
+    T = (1 << 28) + 4099  # 16 tokens a block of 256 threads
+    gu.banner("rope T=%d" % T)
+    x = torch.ones((T, 1, 2), dtype=torch.float16, device="cuda")
+    x[:, 0, 1] = 0
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[None] % 3
+    y = torch.full_like(x, 9.0)
+    wq.wq_rope_dev(wq.wq_rope_create(2, 0, 1e4, [1]), x, pos, y)
+    want = torch.tensor([[np.cos(p), np.sin(p)] for p in range(3)]).half().cuda()
+    wrong = 0
+    for first in range(0, T, 1 << 26):
+        got = y[first:first + (1 << 26), 0]
+        wrong += int(((got - want[pos[0, first:first + (1 << 26)].long()]).abs() > 2.0 ** -10).sum())
+    assert wrong == 0
+
+
+def test_norm_of_many_rows():
+    rows, n = 6_200_000, 16392  # 704 threads a row
+    gu.banner("norm %d x %d" % (rows, n))
+    g = torch.Generator("cuda").manual_seed(1)
+    buf = torch.randn(8 * rows + n, device="cuda", generator=g).bfloat16()
+    x = buf.as_strided((rows, n), (8, 1))
+    w = torch.ones(n, device="cuda")
+    y = torch.empty((1, n), dtype=torch.int8, device="cuda").expand(rows, n)  # the scales are what is looked at
+    sc = torch.full((rows,), float("nan"), device="cuda")
+    wq.wq_rmsnorm_dev(x, w, 1e-6, y, y_scale=sc)
+    torch.cuda.synchronize()
+    assert not sc.isnan().any()
+    for r in [0, 1, (1 << 32) // 704 - 1, (1 << 32) // 704, (1 << 32) // 704 + 1, rows - 1]:
+        t = x[r].double()
+        want = float(t.abs().max() / (t.square().mean() + 1e-6).sqrt() / 127)
+        assert abs(float(sc[r]) - want) <= 38 * U * want, r
+
+
+def test_append_of_many_tokens():
+    """Keys that are not aligned for wide loads: 32 threads a row. All pages but the last are not there."""
+    heads, D, page = 4, 256, 1 << 20
+    T = (1 << 24) + 3
+    gu.banner("append T=%d" % T)
+    g = torch.Generator("cuda").manual_seed(2)
+    buf = torch.randn(8 * T + heads * D + 8, device="cuda", generator=g).half()
+    k, v = (buf.as_strided((T, heads, D), (8, D, 1), off) for off in (1, 3))
+    pools = [torch.zeros((1, heads, page, D // 2), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.zeros((1, heads, page), device="cuda") for _ in "kv"]
+    cache = wq.KvCache(ref.I4, *pools, *scales)
+    table = torch.full((1, 17), -1, dtype=torch.int32, device="cuda")
+    table[0, 16] = 0
+    start, lens = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, T], [T]))
+    wq.wq_kv_append_dev(cache, wq.KvBatch(start, lens, table, T), k, v)
+    torch.cuda.synchronize()
+    for x, pool, sc in zip((k, v), pools, scales):
+        rows, scale = ref.quantise(x[1 << 24:].float().cpu().numpy(), ref.I4)
+        np.testing.assert_array_equal(pool[0, :, :3].cpu().numpy(), rows.transpose(1, 0, 2))
+        np.testing.assert_array_equal(sc[0, :, :3].cpu().numpy(), scale.T)
+        assert not pool[0, :, 3:].any() and not sc[0, :, 3:].any()
+
+
+def test_attention_of_too_many_tiles_is_refused():
+    B = 1 << 24  # a tile a sequence at least, 256 threads a tile
+    start = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    start[-1] = 1
+    lens, table = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    pools = [torch.zeros((1, 1, 16, 64), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    cache = wq.KvCache(ref.I8, *pools, *(torch.zeros((1, 1, 16), device="cuda") for _ in "kv"))
+    q = torch.zeros((1, 1, 64), device="cuda")
+    with pytest.raises(wq.WqError) as e:
+        wq.wq_attn_paged_dev(cache, wq.KvBatch(start, lens, table, 1, max_q=1, max_kv=1), q, torch.empty_like(q), scale=1.0)
+    assert e.value.code == wq.WQ_E_UNSUPPORTED

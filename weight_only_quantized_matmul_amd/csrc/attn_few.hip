@@ -574,7 +574,8 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
 template <typename T, int KIND, int D, int MT>
 hipError_t launch_few(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
     const long blocks = tile_count(a.b.T, a.H / a.c.heads, 16 * MT, a.b.B) * p.nsplit * a.c.heads;
-    if (blocks > 0x7fffffffL || p.rows != 16 * MT || p.step != Few<T, KIND, D, MT>::TK) return hipErrorInvalidValue;
+    if (p.rows != 16 * MT || p.step != Few<T, KIND, D, MT>::TK) return hipErrorInvalidValue;
+    if (blocks > kMaxThreads / 256) return hipErrorNotSupported;
     const dim3 grid((unsigned)blocks), block(256);
     if (wide)
         hipLaunchKernelGGL((attn_few_kernel<T, KIND, D, MT, uint64_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, const 
 template <typename T, int D>
 hipError_t launch_d(const AttnArgs &a, const AttnPlan &p, const Partials &pt, hipStream_t st) {
     const long rows = (long)a.b.T * a.H;
-    if (rows > 0x7fffffffL) return hipErrorInvalidValue;
+    if (rows > kMaxThreads / 256) return hipErrorNotSupported;
     const dim3 block(256);
     // enough partial rows in flight for all splits, at most eight a wave
     if (rows >= 1024 && pt.nsplit <= 16)

@@ -587,7 +587,8 @@ template <typename T, int KIND, int D, int NW>
 hipError_t launch_nw(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
     typedef Tiled<T, KIND, D, NW> F;
     const long blocks = tile_count(a.b.T, a.H / a.c.heads, F::R, a.b.B) * p.nsplit * a.c.heads;
-    if (blocks > 0x7fffffffL || p.rows != F::R) return hipErrorInvalidValue;
+    if (p.rows != F::R) return hipErrorInvalidValue;
+    if (blocks > kMaxThreads / F::NT) return hipErrorNotSupported;
     const dim3 grid((unsigned)blocks), block(F::NT);
     if (wide)
         hipLaunchKernelGGL((attn_tiled_kernel<T, KIND, D, NW, uint64_t>), grid, block, 0, st, a, pt, vec ? 1 : 0);

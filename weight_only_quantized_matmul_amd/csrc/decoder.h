@@ -25,6 +25,11 @@ int begin_call(int device);                                                    /
 int stream_workspace(int device, size_t bytes, hipStream_t st, void **out);    // the stream's workspace
 int device_cus(int device);
 
+// A dimension of a launch holds fewer than 2^32 threads; the runtime does not refuse more, it runs what is left of
+// their number modulo 2^32. Longer work is launched in pieces or laid over a second dimension, or refused
+// (hipErrorNotSupported, WQ_E_UNSUPPORTED to the caller).
+constexpr long kMaxThreads = (1L << 32) - 1;
+
 // ---------------------------------------------------------------------------
 struct NormArgs {
     const void *x, *res;

@@ -19,7 +19,9 @@ struct DeviceScope { // makes `dev` current, restoring the caller's device after
     }
 };
 
-int status(hipError_t e) { return e == hipSuccess ? WQ_OK : e == hipErrorOutOfMemory ? WQ_E_OOM : WQ_E_HIP; }
+int status(hipError_t e) {
+    return e == hipSuccess ? WQ_OK : e == hipErrorOutOfMemory ? WQ_E_OOM : e == hipErrorNotSupported ? WQ_E_UNSUPPORTED : WQ_E_HIP;
+}
 
 bool float_type(int t) { return t >= WQ_DT_F32 && t <= WQ_DT_F16; }
 

@@ -52,7 +52,7 @@ template <int LANES, int RPG>
 __device__ __forceinline__ Where token_of(const KvCopyArgs &a) {
     Where w;
     const unsigned parts = (2 * a.c.heads + RPG - 1) / RPG;
-    const unsigned r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const unsigned r = (blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
     const unsigned tok = r / parts;
     w.any = tok < (unsigned)a.b.T;
     w.tok = w.any ? (int)tok : 0;
@@ -204,7 +204,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const KvCopyArgs a) {
 template <typename T, int KIND, int D, bool VEC, int RPG>
 hipError_t launch_rpg(const KvCopyArgs &a, bool write, hipStream_t st) {
     const long groups = (long)a.b.T * ((2 * a.c.heads + RPG - 1) / RPG);
-    const dim3 grid((unsigned)((groups * (D / 8) + kThreads - 1) / kThreads)), block(kThreads);
+    const long blocks = (groups * (D / 8) + kThreads - 1) / kThreads, gy = (blocks + kMaxThreads / kThreads - 1) / (kMaxThreads / kThreads);
+    const dim3 grid((unsigned)((blocks + gy - 1) / gy), (unsigned)gy), block(kThreads);
     if (write)
         hipLaunchKernelGGL((kv_append_kernel<T, KIND, D, VEC, RPG>), grid, block, 0, st, a);
     else

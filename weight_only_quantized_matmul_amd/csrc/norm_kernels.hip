@@ -211,22 +211,36 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     // 16 waves a CU then hold a row each and the next one's loads
     const long most = (long)cus * (1024 / nt);
     const bool loop = nt <= 512 && a.rows > most;
-    const dim3 grid((unsigned)(loop ? most : a.rows)), block((unsigned)nt);
-    switch (nv) {
+    const int piece = (int)(kMaxThreads / nt); // rows a launch where a block takes one row
+    for (long done = 0; done < a.rows; done += piece) {
+        NormArgs b = a;
+        if (!loop && a.rows > piece) {
+            b.x = (const TX *)a.x + done * a.xs;
+            b.res = a.res ? (const TX *)a.res + done * a.rs : nullptr;
+            b.y = (TY *)a.y + done * a.ys;
+            b.sum = a.sum ? (TX *)a.sum + done * a.ss : nullptr;
+            b.y_scale = a.y_scale ? a.y_scale + done : nullptr;
+            b.rows = (int)(a.rows - done < piece ? a.rows - done : piece);
+        }
+        const dim3 grid((unsigned)(loop ? most : b.rows)), block((unsigned)nt);
+        switch (nv) {
 #define WQ_NV(N)                                                                                                       \
     case N:                                                                                                            \
         if constexpr (N <= LAST) {                                                                                     \
             if (loop)                                                                                                  \
-                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, true>), grid, block, 0, st, a);                \
+                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, true>), grid, block, 0, st, b);                \
             else                                                                                                       \
-                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, false>), grid, block, 0, st, a);               \
+                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, false>), grid, block, 0, st, b);               \
         }                                                                                                              \
         break;
-        WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8)
+            WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8)
 #undef WQ_NV
-    default: return hipErrorInvalidValue;
+        default: return hipErrorInvalidValue;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || loop) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 template <typename TX>

@@ -101,6 +101,19 @@ hipError_t launch_t(RopeArgs &a, bool vec, int cus, hipStream_t st) {
     long tb = 4 * kThreads / items;
     tb = tb < a.T / (2 * cus) ? tb : a.T / (2 * cus);
     a.tb = (int)(tb < 1 ? 1 : tb > kMaxTb ? kMaxTb : tb);
+    const long piece = kMaxThreads / kThreads * a.tb; // tokens a launch
+    if (a.T > piece) {
+        for (long done = 0; done < a.T; done += piece) {
+            RopeArgs b = a;
+            b.x = (const T *)a.x + done * a.xt;
+            b.y = (T *)a.y + done * a.yt;
+            b.pos = a.pos + done;
+            b.T = (int)(a.T - done < piece ? a.T - done : piece);
+            const hipError_t e = launch_t<T>(b, vec, cus, st);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const long gx = (a.T + a.tb - 1) / a.tb;
     // few tokens: the heads are split among blocks, which then turn the same angles again
     long gy = gx >= 2 * cus ? 1 : (2 * cus + gx - 1) / gx;
