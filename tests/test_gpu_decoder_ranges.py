@@ -1,0 +1,67 @@
+"""Inputs far from one: the operators between a decoder layer's products keep their results over fp32's whole range.
+
+Bounds as in test_gpu_decoder.py (u = 2^-24, h(t) half a step of the output type): a norm's output is within
+(36 u + h(t)) |y|, its int8 scale within 38 u of max|y| / 127; codes are exact."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - CPU hosts
+    pytest.skip("no GPU", allow_module_level=True)
+
+import gpu_util as gu  # noqa: E402
+import weight_only_quantized_matmul_amd as wq  # noqa: E402
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": U, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+SMALL = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -25}  # half a step next to zero
+
+
+@pytest.fixture(scope="module", autouse=True)
+def device():
+    gu.reinit_with_env(WQ_FORCE_PATH=None, WQ_FAULT=None, WQ_MEM_LIMIT_BYTES=None)
+    yield
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def norm_and_check(x, w, eps, out, residual=None):
+    rows, n = x.shape
+    y = torch.empty((rows, n), dtype=torch.int8 if out == "i8" else DT[out], device="cuda")
+    sc = torch.full((rows,), 5.0, device="cuda") if out == "i8" else None
+    wq.wq_rmsnorm_dev(x, w, eps, y, residual=residual, y_scale=sc)
+    torch.cuda.synchronize()
+    t, w64 = f64(x if residual is None else x.float() + residual.float()), f64(w)
+    with np.errstate(invalid="ignore"):  # a row of zeros without eps is 0 / 0
+        want = t / np.sqrt((t * t).mean(1, keepdims=True) + float(np.float32(eps))) * w64
+    if out != "i8":
+        none = np.isnan(want)
+        assert np.array_equal(np.isnan(f64(y)), none)
+        assert (np.abs(f64(y) - want) <= (36 * U + 1.01 * HALF[out]) * np.abs(want) + SMALL[out])[~none].all()
+        return
+    tw = t * w64
+    top = np.abs(tw).max(1, keepdims=True)
+    assert np.array_equal(y.cpu().numpy(), np.rint(tw * 127 / np.where(top == 0, 1, top)))
+    scale = np.where(top[:, 0] == 0, 0, np.abs(want).max(1) / 127)
+    assert (np.abs(f64(sc) - scale) <= 38 * U * scale + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("rows,n", [(3, 300), (3, 9001), (2051, 1000)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_rows_of_zeros(rows, n, eps):
+    """Codes and scale of a row of zeros are 0, its neighbours' what they are; NaN rows keep their NaN scale."""
+    x = torch.randn((rows, n), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    x[1] = 0
+    x[rows - 1] = 0
+    norm_and_check(x, torch.ones(n, device="cuda"), eps, "i8")
+    x[1, n - 1] = float("nan")
+    y, sc = torch.full((rows, n), 9, dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda")
+    wq.wq_rmsnorm_dev(x, torch.ones(n, device="cuda"), eps, y, y_scale=sc)
+    assert sc[1].isnan() and not y[1].any() and sc[0] > 0 and sc[rows - 1] == 0

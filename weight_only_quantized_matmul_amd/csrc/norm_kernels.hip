@@ -163,7 +163,7 @@ __global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormAr
                 store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         } else {
-            const float scale = (float)(top * (double)rstd / 127.0);
+            const float scale = sq == 0.f ? 0.f : (float)(top * (double)rstd / 127.0); // zeros without eps: rstd is infinite
             if (tid == 0) a.y_scale[row] = scale;
             // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
             const bool ok = top > 0.0 && scale == scale;
