@@ -377,7 +377,8 @@ enum wq_dtype { WQ_DT_F32 = 0, WQ_DT_BF16 = 1, WQ_DT_F16 = 2, WQ_DT_I8 = 3 };
  * floats): y_scale = max|y| / 127 and the codes are
  * rint(127 * (r*w) / max|r*w|), the quotient in fp64, so y ~ code * y_scale;
  * a row of zeros gets codes 0 and scale 0, a row holding an infinity or a
- * NaN codes 0 and a NaN scale. sum_out may be x or residual (same stride), and
+ * NaN codes 0 and a NaN scale. Finite rows of any size have finite squares
+ * here (in float types a row of zeros with eps 0 is 0 / 0, a NaN). sum_out may be x or residual (same stride), and
  * y may be x when the types and strides agree.
  * n <= WQ_NORM_MAX_N (WQ_E_UNSUPPORTED above); rows == 0 is a no-op.
  */

@@ -65,3 +65,27 @@ def test_norm_rows_of_zeros(rows, n, eps):
     y, sc = torch.full((rows, n), 9, dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda")
     wq.wq_rmsnorm_dev(x, torch.ones(n, device="cuda"), eps, y, y_scale=sc)
     assert sc[1].isnan() and not y[1].any() and sc[0] > 0 and sc[rows - 1] == 0
+
+
+EXPONENTS = (-146, -126, -100, -70, -64, -60, -50, 0, 50, 60, 63, 64, 70, 100, 124)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16", "i8"])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("rows,n", [(len(EXPONENTS), 300), (len(EXPONENTS), 40), (len(EXPONENTS), 20001), (3003, 1000)])
+def test_norm_rows_of_any_size(dtype, out, eps, rows, n):
+    """Rows of every size beside each other, in one call: each decides by itself how its squares are summed."""
+    gu.banner("norm sizes %s -> %s eps=%g %d x %d" % (dtype, out, eps, rows, n))
+    rng = np.random.default_rng(rows + n)
+    e = np.resize(EXPONENTS, rows)[:, None]
+    x = torch.from_numpy(np.ldexp(rng.uniform(0.5, 1.5, (rows, n)) * rng.choice([-1, 1], (rows, n)), e).astype(np.float32))
+    norm_and_check(x.cuda().to(DT[dtype]), torch.from_numpy(rng.uniform(0.5, 2, n).astype(np.float32)).cuda(), eps, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "i8"])
+def test_norm_sums_of_any_size(out):
+    rng = np.random.default_rng(9)
+    x, r = (torch.from_numpy(np.ldexp(rng.normal(size=(6, 500)), np.array([[-100], [0], [64], [100], [-64], [120]])).astype(np.float32)).cuda()
+            for _ in range(2))
+    norm_and_check(x, torch.ones(500, device="cuda"), 0.0, out, residual=r)

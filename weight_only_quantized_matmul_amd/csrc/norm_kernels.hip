@@ -74,7 +74,7 @@ __device__ __forceinline__ void store_row(T *p, int left, const float *v) {
 template <typename TX, typename TY, int VEC, int NV, bool ANY, bool LOOP>
 __global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormArgs a) {
     constexpr bool CODE = IsCode<TY>::value;
-    __shared__ float red[2][16]; // of odd and even rows: one barrier a row
+    __shared__ float red[2][16], red_far[16]; // red: of odd and even rows, one barrier a row
     __shared__ double red64[2][16];
     const int tid = threadIdx.x, nt = blockDim.x, n = a.n;
     typename Vec<TX, VEC>::type nx[NV], nr[NV];
@@ -143,7 +143,37 @@ __global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormAr
                 if (CODE) top = fmax(top, red64[buf][i]);
             }
         }
-        const float rstd = 1.0f / sqrtf(sq / (float)n + a.eps);
+        // Squares overflow from elements of about 2^56 on and lose those below 2^-63. Rows whose sum shows either (all
+        // threads see the same sum) are taken up or down by a power of two first, and eps with them: the products stay
+        // exact, and every fp32 row then has its squares between 2^-118 and 2^121.
+        float ms = sq / (float)n + a.eps, up = 1.f;
+        if (__builtin_amdgcn_readfirstlane(!(ms < INFINITY) || (sq < 0x1p-80f && a.eps < 0x1p-60f))) {
+            up = ms < INFINITY ? 0x1p90f : 0x1p-75f;
+            sq = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sq = fmaf(v[j][i] * up, v[j][i] * up, sq);
+#pragma unroll
+            for (int m = 32; m > 0; m >>= 1) sq += __shfl_xor(sq, m);
+            if (nt > 64) {
+                if ((tid & 63) == 0) red_far[tid >> 6] = sq;
+                __syncthreads(); // between these reads and the next row's writes stands that row's first barrier
+                sq = 0.f;
+                for (int i = 0; i < nt >> 6; ++i) sq += red_far[i];
+            }
+            ms = sq / (float)n + a.eps * up * up;
+        }
+        const float rstd = 1.0f / sqrtf(ms); // of the row times `up`
+        // Products and fp64 forms made for the maximum are made again below where they would spill: 8 loads of 20000 bf16
+        // to int8 31.5 us, kept 35.7. The row-walking form does best with most of them (74 us for 8191 x 6144, made again 81),
+        // but for the last load's of its longest rows (5000 x 8192: 61 us, two registers spilled 67).
+        if (CODE && (!LOOP || NV * VEC >= 32)) {
+#pragma unroll
+            for (int j = LOOP ? NV - 1 : 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) asm volatile("" : "+v"(v[j][i]), "+v"(w[j][i]));
+        }
         if (a.sum) {
             TX *s = (TX *)a.sum + row * a.ss;
 #pragma unroll
@@ -159,11 +189,12 @@ __global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormAr
                 const int e = (j * nt + tid) * VEC;
                 float o[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * rstd * w[j][i];
+                for (int i = 0; i < VEC; ++i) o[i] = v[j][i] * up * rstd * w[j][i];
                 store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         } else {
-            const float scale = sq == 0.f ? 0.f : (float)(top * (double)rstd / 127.0); // zeros without eps: rstd is infinite
+            // a row of zeros without eps has an infinite rstd
+            const float scale = top == 0.0 && sq == sq ? 0.f : (float)(top * (double)up * (double)rstd / 127.0);
             if (tid == 0) a.y_scale[row] = scale;
             // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
             const bool ok = top > 0.0 && scale == scale;
