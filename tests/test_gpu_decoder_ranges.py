@@ -89,3 +89,16 @@ def test_norm_sums_of_any_size(out):
     x, r = (torch.from_numpy(np.ldexp(rng.normal(size=(6, 500)), np.array([[-100], [0], [64], [100], [-64], [120]])).astype(np.float32)).cuda()
             for _ in range(2))
     norm_and_check(x, torch.ones(500, device="cuda"), 0.0, out, residual=r)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("rows,n", [(2, 300), (2500, 1001)])
+def test_norm_infinities_behind_zero_weights(rows, n, bad):
+    """A row is not finite wherever its infinity stands, also where the weight is 0."""
+    x, w = torch.ones((rows, n), device="cuda"), torch.ones(n, device="cuda")
+    w[n // 2] = 0
+    x[rows - 1, n // 2] = bad
+    y, sc = torch.full((rows, n), 9, dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda")
+    wq.wq_rmsnorm_dev(x, w, 1e-6, y, y_scale=sc)
+    assert sc[rows - 1].isnan() and not y[rows - 1].any()
+    assert (y[:-1, : n // 2] == 127).all() and (y[:-1, n // 2] == 0).all() and (sc[:-1] > 0).all()

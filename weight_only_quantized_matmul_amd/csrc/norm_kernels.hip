@@ -193,10 +193,9 @@ __global__ __launch_bounds__(LOOP ? 512 : 1024) void rmsnorm_kernel(const NormAr
                 store_row<TY, VEC, ANY>(y + e, n - e, o);
             }
         } else {
-            // a row of zeros without eps has an infinite rstd
-            const float scale = top == 0.0 && sq == sq ? 0.f : (float)(top * (double)up * (double)rstd / 127.0);
+            // sq is finite where the row is, whatever its weights hide; a row of zeros without eps has an infinite rstd
+            const float scale = !(sq < INFINITY) ? NAN : top == 0.0 ? 0.f : (float)(top * (double)up * (double)rstd / 127.0);
             if (tid == 0) a.y_scale[row] = scale;
-            // top = 0: a row of zeros. A NaN scale: an infinity or a NaN in the row.
             const bool ok = top > 0.0 && scale == scale;
             const bool range = top > 1e-30 && top < 1e30; // fp32 holds the products and the quotient's factor
             const double inv64 = 127.0 / top;
