@@ -257,10 +257,11 @@ hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
 #define WQ_NV(N)                                                                                                       \
     case N:                                                                                                            \
         if constexpr (N <= LAST) {                                                                                     \
-            if (loop)                                                                                                  \
-                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, true>), grid, block, 0, st, b);                \
-            else                                                                                                       \
+            if (!loop) {                                                                                               \
                 hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, false>), grid, block, 0, st, b);               \
+            } else if constexpr (N <= 4) { /* eight loads a thread only where 512 threads do not hold the row */       \
+                hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, VEC, N, ANY, true>), grid, block, 0, st, b);                \
+            }                                                                                                          \
         }                                                                                                              \
         break;
             WQ_NV(1) WQ_NV(2) WQ_NV(3) WQ_NV(4) WQ_NV(8)
