@@ -599,7 +599,10 @@ hipError_t launch_nw(const AttnArgs &a, const AttnPlan &p, const Partials &pt, b
 
 template <typename T, int KIND, int D>
 hipError_t launch_d(const AttnArgs &a, const AttnPlan &p, const Partials &pt, bool vec, bool wide, hipStream_t st) {
-    return p.waves == 8 ? launch_nw<T, KIND, D, 8>(a, p, pt, vec, wide, st) : launch_nw<T, KIND, D, 4>(a, p, pt, vec, wide, st);
+    if (p.waves == 4) return launch_nw<T, KIND, D, 4>(a, p, pt, vec, wide, st);
+    if constexpr (D > 64) // rows of 64 always take four waves
+        return launch_nw<T, KIND, D, 8>(a, p, pt, vec, wide, st);
+    return hipErrorInvalidValue;
 }
 
 template <typename T, int KIND>
