@@ -473,14 +473,18 @@ int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_o
  *     o = sum_t w_t v_t,       lse = log sum_t exp(s_t),
  * where t is seen if 0 <= t < kv_len[b], t <= p (causal) and t > p - window
  * (window > 0). A token that sees nothing gets o = 0 and lse = -inf. What
- * unseen positions hold (infinities and NaN among it) never enters a result.
+ * unseen positions hold (infinities and NaN among it) never enters a result;
+ * a seen value's code that is not finite makes its element of o an infinity
+ * or a NaN.
  * q, o: [T, H, dim] of dtype (f32, bf16, f16) with strides; H a multiple of
  * the cache's heads; lse: float [T, H], contiguous, or NULL. The softmax
  * statistics and all sums are fp32; codes enter the matrix units exactly.
- * f32 queries enter as two f16 parts (22 bits and more), their probabilities
- * as three bf16 parts (24 bits) against integer codes and as two f16 parts
- * against f16 codes (22 bits, down to 2^-39 of a row's largest); bf16/f16
- * queries enter exactly, their probabilities rounded to f16 (2^-11).
+ * f32 queries enter as two f16 parts (22 bits and more), 16-bit queries
+ * exactly. Probabilities (times their values' scales) of f32 queries enter as
+ * three bf16 parts (24 bits) against integer codes, and else as two f16 parts
+ * (22 bits, down to 2^-39 of the largest value scale in the row), but for bf16
+ * queries of many rows: one f16 part (2^-11), an eighth of what rounding o to
+ * bf16 leaves.
  * Where the positions are split among blocks, partial results pass through
  * the stream's workspace as in wq_matmul_dev (it may grow; while the stream
  * is being captured it cannot: warm up first, else WQ_E_UNSUPPORTED; a graph

@@ -2,6 +2,8 @@
 // see, how cache codes become f16 operands, and partial results.
 #pragma once
 
+#include <type_traits>
+
 #include "decoder.h"
 
 namespace wq {

@@ -17,10 +17,11 @@
 // A query row is brought to [2^13, 2^14) by a power of two; f32 rows enter as
 // two f16 parts (22 bits and more), 16-bit types exactly as one. A probability
 // times its value's scale enters, for f32 and integer codes, as three bf16
-// parts (all 24 bits, any magnitude; the codes are exact in bf16 too); for f32
-// and f16 codes as two f16 parts, for 16-bit types as one (half a step 2^-11),
-// the exponent of all of a row's probabilities shifted so that times its
-// largest value scale so far they stay below 2^14.
+// parts (all 24 bits, any magnitude; the codes are exact in bf16 too); else as
+// two f16 parts (22 bits; with one, 2^-11, f16 outputs were 1.4 times as far
+// from 64 bits and the batch below 1 us faster), the exponent of all of a row's
+// probabilities shifted so that times its largest value scale so far they stay
+// below 2^14.
 //
 // Next to the bytes the opening of codes is what costs: K's and V's of a step
 // are about 370 of its 850 vector instructions in int4. 64 ragged sequences up to
@@ -37,7 +38,7 @@ struct Few {
     static constexpr int EPB2 = KIND == WQ_KV_F16 ? 1 : KIND == WQ_KV_I8 ? 2 : 4;       // codes per two bytes
     static constexpr int P = sizeof(T) == 4 ? 2 : 1;                                    // f16 parts of q
     static constexpr bool BF = P == 2 && KIND != WQ_KV_F16;                             // p and v in bf16
-    static constexpr int PP = BF ? 3 : P;                                               // parts of p
+    static constexpr int PP = BF ? 3 : 2;                                               // parts of p
     static constexpr int TK = RB <= 64 ? 64 : 32;                                      // positions a block
     static constexpr int LB = RB / 4 < 16 ? RB / 4 : 16; // bytes of one K load
     static constexpr int KL = RB / 4 / LB;               // K loads a lane and key

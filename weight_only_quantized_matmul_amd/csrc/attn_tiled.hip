@@ -12,7 +12,12 @@
 // elements, whose operands would not fit the registers otherwise). A lane
 // holds quads of four consecutive keys of one row in S^T; V's columns stand in
 // LDS in the order in which these quads form P^T operands, so probabilities
-// never leave their lane. Parts and scales are as in the few-rows kernel.
+// never leave their lane. Parts and scales are as in the few-rows kernel, but
+// for bf16 queries, whose probabilities enter as one f16 part (2^-11): the prompt
+// below takes 202 us so, 245 and more with two, and rounding the output to bf16
+// leaves eight times as much (error against 64 bits 1.672e-3 of the root mean
+// square, with exact probabilities 1.658e-3). f16 outputs show it (2.98e-4
+// against 2.08e-4), so f16 queries take two parts: that prompt in 259 us.
 //
 // Bound by the vector units and the matrix units in turn (the softmax costs six
 // instructions and an exponential an element). 4096 tokens, causal, 32 heads over
@@ -61,7 +66,7 @@ struct Tiled {
     static constexpr int KBH = KBN / HV, NQH = NQ / HV, STH = ST / HV;
     static constexpr int P = sizeof(T) == 4 ? 2 : 1; // f16 parts of q
     static constexpr bool BF = P == 2 && KIND != WQ_KV_F16;
-    static constexpr int PP = BF ? 3 : P;            // parts of p
+    static constexpr int PP = BF ? 3 : sizeof(T) == 4 || std::is_same<T, f16>::value ? 2 : 1;            // parts of p
     static constexpr int KU = TK * CH / NT;          // 8-code units of K a thread brings
     static constexpr int KW = KIND == WQ_KV_F16 ? 4 : KIND == WQ_KV_I8 ? 2 : 1; // words of one
     static constexpr int DG = TK * 32 / NT >= 4 ? 32 : 64; // parts of a V row
@@ -260,7 +265,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     auto store_v = [&](int buf, int step, uint64_t mask, bool edge) {
         if constexpr (KIND == WQ_KV_F16) {
             // An infinity or a NaN among the codes must not reach rows that do not see it (0 * NaN):
-            // where rows differ in what they see, such codes leave the operands and are taken one by one.
+            // where rows differ in what they see, such codes leave the operands and are looked up at the end.
             if (edge) {
                 bool bad = false;
 #pragma unroll
@@ -388,11 +393,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     }
     __syncthreads();
 
+    int bad_from = blk1, bad_to = blk0; // steps that codes were taken out of
     for (int i = blk0; i < blk1; ++i) {
         const int c = i - blk0, buf = c & 1, t0 = sp.base + i * TK;
         const uint64_t mask = s_mask[c & 3], mask_next = s_mask[(c + 1) & 3];
         const float big_all = F::BF ? 0.f : s_big[buf];
-        const int bad_now = KIND == WQ_KV_F16 ? s_bad[c % 3] : 0;
+        if (KIND == WQ_KV_F16 && s_bad[c % 3]) {
+            bad_from = min(bad_from, i);
+            bad_to = i + 1;
+        }
         fetch_k(s_off[(c + 1) & 3]); // past the last step: row 0 again, unused
         fetch_v(s_off[(c + 1) & 3]);
         Key key2;
@@ -467,32 +476,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
                     for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], 0.f);
             }
             l = l * grow + sum;
-            if constexpr (KIND == WQ_KV_F16) {
-                if (bad_now) {
-                    for (int key = h * (TK / F::HV); key < (h + 1) * (TK / F::HV); ++key) {
-                        if (!(mask >> key & 1)) continue;
-                        // the row's offset is no longer in LDS: look it up again
-                        const int pos = t0 + key, idx = page_index(a.c, pos);
-                        const f16 *src = (const f16 *)(vp + ((OFF)table[idx] * (OFF)a.c.rp + (OFF)(pos - idx * a.c.page) * (OFF)a.c.rs));
-                        float y = 0.f;
-#pragma unroll
-                        for (int j = 0; j < F::NQH; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (j == key / (4 * NG) - h * F::NQH && e == (key & 3)) y = s[j / F::QB][4 * (j % F::QB) + e];
-                        y = __shfl(y, (key >> 2 & (NG - 1)) * RW + n);
-                        if (pos >= row_lo && pos < row_hi) {
-#pragma unroll
-                            for (int d = 0; d < F::DB; ++d)
-#pragma unroll
-                                for (int k = 0; k < 4 * F::QB; ++k) {
-                                    const float code = (float)src[d * RW + 4 * NG * (k >> 2) + 4 * g + (k & 3)];
-                                    if (!(fabsf(code) < INFINITY)) o[d][k] = fmaf(y, code, o[d][k]);
-                                }
-                        }
-                    }
-                }
-            }
             constexpr int N = VN;
             __builtin_amdgcn_s_setprio(1);
             f16x8 fr[VAHEAD];
@@ -544,6 +527,26 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     }
 
     if (!working) return;
+    if constexpr (KIND == WQ_KV_F16) {
+        // Codes that are not finite and were taken out: what sees one is not finite either, whatever else it sums. Here
+        // and not in the step, where this loop's registers would add to all the others (8 spilled, 52 with two parts).
+        const int last = min(sp.base + bad_to * TK, w_hi);
+        for (int pos = max(sp.base + bad_from * TK, w_lo); bad_from < bad_to && pos < last; ++pos) {
+            const int idx = page_index(a.c, pos), page = table[idx], slot = pos - idx * a.c.page;
+            if (page < 0 || page >= a.c.pages) continue;
+            const f16 *src = (const f16 *)(vp + ((OFF)page * (OFF)a.c.rp + (OFF)slot * (OFF)a.c.rs));
+            const float scale = vsp[(OFF)page * (OFF)a.c.sp + (OFF)slot * (OFF)a.c.ss];
+            if (pos >= row_lo && pos < row_hi) {
+#pragma unroll
+                for (int d = 0; d < F::DB; ++d)
+#pragma unroll
+                    for (int k = 0; k < 4 * F::QB; ++k) {
+                        const float code = (float)src[d * RW + 4 * NG * (k >> 2) + 4 * g + (k & 3)];
+                        if (!(fabsf(code) < INFINITY)) o[d][k] = fmaf(scale, code, o[d][k]);
+                    }
+            }
+        }
+    }
     l = row_sum<NG>(l);
     if (!live) return;
     const long at = (long)(t.tok0 + tok) * a.H + head;
