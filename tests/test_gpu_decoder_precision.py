@@ -65,3 +65,28 @@ def test_f16_codes_that_are_not_finite(dtype, D, q_len):
         bad[(p >= t) & (p < t + window), :, d] = True
     assert torch.equal(~o2[:, 2:].isfinite(), bad)  # an infinity or, where parts of a probability differ in sign, a NaN
     assert torch.equal(o2[:, 2:][~bad], o[:, 2:][~bad])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", [ref.F16, ref.I8])
+@pytest.mark.parametrize("first", [0.0, 2.0 ** -60, 2.0 ** 60])
+@pytest.mark.parametrize("q_len,kv_len,border", [([1], 300, 150), ([1], 6000, 3000), ([90], 700, 350), ([200], 3000, 1500)])
+def test_value_scales_that_differ_widely(dtype, kind, first, q_len, kv_len, border):
+    """Rows of zeros, or of values 2^120 apart, in one context: every position keeps its weight in the softmax, within a
+    step, between the waves of a block and between splits."""
+    gu.banner("value scales %s kind=%d first=%g q=%s kv=%d" % (dtype, kind, first, q_len, kv_len))
+    c = Case(kv_len + kind, kind, 64, 1, 16, q_len, [kv_len])
+    vs = c.dev[3].cpu()
+    for t in range(kv_len):
+        pg, slot = ref.place_at(c.table, c.pages, 16, 0, t)
+        vs[pg, 0, slot] *= first if t < border else (2.0 ** -60 if first > 1 else 2.0 ** 60)
+    c.dev[3].copy_(vs)
+    q = queries(c, 4, dtype, 0.3)
+    o, l = attend(c, q, dtype)
+    want, lse, A, S = ref.attention(f64(q), kind, *c.host(), c.q_start, c.kv_len, c.table, 64 ** -0.5, True, 0)
+    e = (64 + 8) * U * S
+    r = 2.0 ** -21 if dtype == "f32" or q_len[0] == 1 else 2 * 2.0 ** -11
+    tol = A * (2 * e + (kv_len + 72) * U + r)[..., None] + 1.01 * HALF[dtype] * np.abs(want) + SMALL[dtype]
+    err = np.abs(f64(o) - want)
+    assert (err <= tol).all(), "%d of %d off, worst %.3g of the bound" % ((err > tol).sum(), err.size, np.nanmax(err / tol))
+    assert (np.abs(f64(l) - lse) <= e + (kv_len + 72) * U + U * np.abs(lse) + U).all()

@@ -241,6 +241,11 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t *o) {
     o[2] = high_halves(a, b);
 }
 
+// 2^(x/2): sums of probabilities are rescaled by 2^x in two steps. Exponents of partial sums differ by up to 217 (values'
+// scales from 2^-90 to 2^127), and 2^x alone is 0 below 2^-126, where the sum still counts. The values' sums do not need it:
+// what they lose then is below 2^-126 of the largest scale.
+__device__ __forceinline__ float half_way(float x) { return __builtin_amdgcn_exp2f(0.5f * x); }
+
 // Two floats rounded to halves (to nearest), in one register.
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const f32x2 v = {a, b};

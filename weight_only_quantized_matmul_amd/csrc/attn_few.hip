@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
             const float was = ref[mt];
             ref[mt] = m[mt] == -INFINITY ? -INFINITY : m[mt] - e_min[mt];
             const float base = m[mt] == -INFINITY ? 0.f : ref[mt];
-            const float grow = __builtin_amdgcn_exp2f(was - base);
+            const float grow = half_way(was - base);
             float sum = 0.f;
 #pragma unroll
             for (int kb = 0; kb < F::KB; ++kb) {
@@ -339,10 +339,10 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
                     }
                 }
             }
-            l[mt] = l[mt] * grow + sum;
+            l[mt] = l[mt] * grow * grow + sum;
             if (__ballot(grow != 1.f)) {
 #pragma unroll
-                for (int d = 0; d < F::DT; ++d) o[mt][d] *= grow;
+                for (int d = 0; d < F::DT; ++d) o[mt][d] *= grow * grow;
             }
         }
 
@@ -498,7 +498,10 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
         const float base = M[mt] == -INFINITY ? 0.f : M[mt];
         L[mt] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) L[mt] += sh_l[w][r] * __builtin_amdgcn_exp2f(sh_m[w][r] - base);
+        for (int w = 0; w < 4; ++w) {
+            const float h = half_way(sh_m[w][r] - base);
+            L[mt] += sh_l[w][r] * h * h;
+        }
         const float f = __builtin_amdgcn_exp2f(ref[mt] - base) * (F::BF && KIND == WQ_KV_I4 ? 16.f : 1.f);
 #pragma unroll
         for (int d = 0; d < F::DT; ++d) o[mt][d] *= f;

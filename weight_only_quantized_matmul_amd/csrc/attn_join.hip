@@ -80,10 +80,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, const 
 #pragma unroll
         for (int k = 0; k < AT; ++k) {
             const bool on = first + WPR * k < sp.splits; // what stands past the splits is not looked at
-            const float f = on ? __builtin_amdgcn_exp2f(r[k] - base) : 0.f;
-            L = on ? fmaf(l[k], f, L) : L;
+            const float f = on ? half_way(r[k] - base) : 0.f;
+            L = on ? fmaf(l[k] * f, f, L) : L;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = on ? fmaf(v[k][e], f, o[e]) : o[e];
+            for (int e = 0; e < E; ++e) o[e] = on ? fmaf(v[k][e], f * f, o[e]) : o[e];
         }
     }
     if constexpr (WPR > 1) {

@@ -454,9 +454,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
                 m = moves ? fmaxf(m, now) : m;
                 e_min = moves ? room : e_min;
                 ref = m == -INFINITY ? -INFINITY : m - e_min;
-                grow = __builtin_amdgcn_exp2f(was - (m == -INFINITY ? 0.f : ref));
+                grow = half_way(was - (m == -INFINITY ? 0.f : ref));
 #pragma unroll
-                for (int d = 0; d < F::DB; ++d) o[d] *= grow;
+                for (int d = 0; d < F::DB; ++d) o[d] *= grow * grow;
             }
             const float base = m == -INFINITY ? 0.f : ref;
             float sum = 0.f;
@@ -475,7 +475,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[j / F::QB][4 * (j % F::QB) + e] = where_seen(sees, 4 * NG * j + e, s[j / F::QB][4 * (j % F::QB) + e], 0.f);
             }
-            l = l * grow + sum;
+            l = l * grow * grow + sum;
             constexpr int N = VN;
             __builtin_amdgcn_s_setprio(1);
             f16x8 fr[VAHEAD];
