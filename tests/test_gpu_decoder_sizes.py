@@ -97,3 +97,85 @@ def test_attention_of_too_many_tiles_is_refused():
     with pytest.raises(wq.WqError) as e:
         wq.wq_attn_paged_dev(cache, wq.KvBatch(start, lens, table, 1, max_q=1, max_kv=1), q, torch.empty_like(q), scale=1.0)
     assert e.value.code == wq.WQ_E_UNSUPPORTED
+
+
+def far_context(new):
+    """A context of 2^31 - 1 positions: one page of 2^20 slots, 2048 times."""
+    page, D = 1 << 20, 64
+    g = torch.Generator("cuda").manual_seed(7)
+    pools = [torch.randint(0, 256, (1, 1, page, D // 2), dtype=torch.uint8, device="cuda", generator=g) for _ in "kv"]
+    scales = [0.05 + 0.05 * torch.rand((1, 1, page), device="cuda", generator=g) for _ in "kv"]
+    cache = wq.KvCache(ref.I4, *pools, *scales)
+    start, lens = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, new], [(1 << 31) - 1]))
+    batch = wq.KvBatch(start, lens, torch.zeros((1, 2048), dtype=torch.int32, device="cuda"), new, max_q=new, max_kv=(1 << 31) - 1)
+    opened = [ref.open_rows(p.cpu().numpy()[0, 0], ref.I4) * s.cpu().numpy()[0, 0].astype(np.float64)[:, None] for p, s in zip(pools, scales)]
+    q = torch.randn((new, 2, D), device="cuda", generator=g)
+    return cache, batch, q, opened
+
+
+@pytest.mark.parametrize("new,window", [(1, 100), (1, 5000), (9, 70), (90, 300), (300, 6000)])
+def test_last_positions_before_2_to_the_31(new, window):
+    gu.banner("window %d at position 2^31, %d new" % (window, new))
+    cache, batch, q, (K, V) = far_context(new)
+    o, l = torch.empty_like(q), torch.empty((new, 2), device="cuda")
+    wq.wq_attn_paged_dev(cache, batch, q, o, scale=0.125, window=window, lse=l)
+    o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+    for i in range(new):
+        p = (1 << 31) - 1 - new + i
+        at = np.arange(p - window + 1, p + 1) % (1 << 20)
+        for h in range(2):
+            s = 0.125 * (K[at] @ q[i, h].double().cpu().numpy())
+            w = np.exp(s - s.max())
+            A = (w / w.sum()) @ np.abs(V[at])
+            e = 72 * U * 0.125 * (np.abs(K[at]) @ np.abs(q[i, h].double().cpu().numpy())).max()
+            assert (np.abs(o[i, h] - (w / w.sum()) @ V[at]) <= A * (2 * e + (window + 72) * U + 2.0 ** -21) + U * A).all(), i
+            assert abs(l[i, h] - s.max() - np.log(w.sum())) <= e + (window + 72) * U + 30 * U, i
+
+
+def test_all_positions_before_2_to_the_31():
+    """Weights in fp32 sums: a split's chain is 2^31 / 512 positions, 32 or 64 a step and four waves, then the join."""
+    gu.banner("attention over 2^31 - 1 positions")
+    cache, batch, q, (K, V) = far_context(1)
+    o, l = torch.empty_like(q), torch.empty((1, 2), device="cuda")
+    wq.wq_attn_paged_dev(cache, batch, q, o, scale=0.125, lse=l)
+    o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+    n = np.full(1 << 20, 2048.0)
+    n[-1] = 2047
+    for h in range(2):
+        s = 0.125 * (K @ q[0, h].double().cpu().numpy())
+        w = n * np.exp(s - s.max())
+        A = (w / w.sum()) @ np.abs(V)
+        e = 72 * U * 0.125 * (np.abs(K) @ np.abs(q[0, h].double().cpu().numpy())).max()
+        chain = (1 << 31) // 512 // 128 + 512
+        assert (np.abs(o[0, h] - (w / w.sum()) @ V) <= A * (2 * e + 2 * chain * U + 2.0 ** -21)).all()
+        assert abs(l[0, h] - s.max() - np.log(w.sum())) <= e + chain * U + 40 * U
+
+
+def test_append_at_the_last_position():
+    cache, batch, _, _ = far_context(1)
+    k, v = (torch.randn((1, 1, 64), device="cuda", generator=torch.Generator("cuda").manual_seed(i)) for i in (1, 2))
+    was = [t.clone() for t in cache.tensors]
+    wq.wq_kv_append_dev(cache, batch, k, v)
+    back = [torch.empty_like(k) for _ in "kv"]
+    wq.wq_kv_read_dev(cache, batch, *back)
+    for x, b, pool, sc, p0, s0 in zip((k, v), back, cache.tensors[:2], cache.tensors[2:], was[:2], was[2:]):
+        rows, scale = ref.quantise(x.cpu().numpy(), ref.I4)
+        p0[0, 0, (1 << 20) - 2], s0[0, 0, (1 << 20) - 2] = torch.from_numpy(rows[0, 0]).cuda(), float(scale[0, 0])
+        assert torch.equal(pool, p0) and torch.equal(sc, s0)
+        np.testing.assert_array_equal(b.cpu().numpy()[0, 0], (ref.open_rows(rows, ref.I4) * scale[..., None]).astype(np.float32)[0, 0])
+
+
+@pytest.mark.parametrize("kv", [-1, -5, -(1 << 31)])
+def test_negative_lengths_are_empty(kv):
+    """No position is there: nothing is written, zeros are read, attention sees nothing."""
+    cache, _, _, _ = far_context(1)
+    start, lens = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, 2], [kv]))
+    batch = wq.KvBatch(start, lens, torch.zeros((1, 2048), dtype=torch.int32, device="cuda"), 2)
+    x, back, q = torch.ones((2, 1, 64), device="cuda"), torch.ones((2, 1, 64), device="cuda"), torch.ones((2, 2, 64), device="cuda")
+    was = [t.clone() for t in cache.tensors]
+    wq.wq_kv_append_dev(cache, batch, x, x)
+    wq.wq_kv_read_dev(cache, batch, back, back)
+    o, l = torch.ones_like(q), torch.ones((2, 2), device="cuda")
+    wq.wq_attn_paged_dev(cache, batch, q, o, scale=0.1, lse=l)
+    assert all(torch.equal(a, b) for a, b in zip(was, cache.tensors))
+    assert not back.any() and not o.any() and (l == -float("inf")).all()

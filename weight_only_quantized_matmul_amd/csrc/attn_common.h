@@ -70,6 +70,11 @@ __device__ __forceinline__ Tile find_tile(const BatchView &b, int page, int G, l
     return t;
 }
 
+// Position `lane` of block i. Past 2^31 - 1 it wraps to a negative number, which no row sees.
+__device__ __forceinline__ int position(int base, int i, int step, int lane) {
+    return (int)((unsigned)base + (unsigned)i * (unsigned)step + (unsigned)lane);
+}
+
 // Positions [lo, hi) that new token i sees.
 __device__ __forceinline__ void seen_range(const Tile &t, int i, int causal, int window, int *lo, int *hi) {
     const long p = (long)t.past + i;
@@ -103,7 +108,7 @@ struct Span {
 __device__ __forceinline__ Span find_span(int step, int lo, int hi, int least, int nsplit) {
     Span s;
     s.base = lo & -step;
-    s.blocks = hi > lo ? (hi - s.base + step - 1) / step : 0;
+    s.blocks = hi > lo ? (int)(((unsigned)(hi - s.base) + (unsigned)step - 1) / (unsigned)step) : 0; // hi up to 2^31 - 1
     const int most = max(least, (s.blocks + nsplit - 1) / nsplit);
     s.splits = max(1, (s.blocks + most - 1) / most);
     s.per = (s.blocks + s.splits - 1) / s.splits; // splits of equal length

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
     };
     auto look = [&](int i) {
         Key k;
-        const int pos = sp.base + i * TK + lane;
+        const int pos = position(sp.base, i, TK, lane);
         k.there = i < blk1 && lane < TK && pos >= lo && pos < hi;
         const int idx = page_index(a.c, pos);
         k.slot = pos - idx * a.c.page;
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(const AttnArgs a, const P
             }
         }
         constexpr uint64_t all = TK == 64 ? ~0ull : 0xffffffffull;
-        const bool edge = mask0 != all || t0 < lo_max || t0 + TK > hi_min;
+        const bool edge = mask0 != all || t0 < lo_max || t0 > hi_min - TK;
         if (edge) { // a key that a row does not see scores -inf there and has scale 0, whatever it held
             const uint64_t own = mask0 >> (4 * g);
 #pragma unroll

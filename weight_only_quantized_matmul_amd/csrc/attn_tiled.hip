@@ -183,7 +183,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     };
     auto look = [&](int i) {
         Key k;
-        const int pos = sp.base + i * TK + lane;
+        const int pos = position(sp.base, i, TK, lane);
         k.there = i < blk1 && (TK == 64 || lane < TK) && pos >= lo && pos < hi;
         const int idx = page_index(a.c, pos);
         k.slot = pos - idx * a.c.page;
@@ -323,8 +323,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     };
     constexpr uint64_t all = TK == 64 ? ~0ull : 0xffffffffull;
     auto is_edge = [&](int i, uint64_t mask) {
-        const int t0 = sp.base + i * TK;
-        return mask != all || t0 < lo_max || t0 + TK > hi_min;
+        const int t0 = position(sp.base, i, TK, 0);
+        return mask != all || t0 < lo_max || t0 > hi_min - TK;
     };
 
     float ref = -INFINITY, m = -INFINITY, l = 0.f; // p = 2^(s - ref)
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
         }
     };
     // does the wave work on step i?
-    auto active = [&](int i) { return working && i < blk1 && sp.base + i * TK < w_hi && sp.base + i * TK + TK > w_lo; };
+    auto active = [&](int i) { return working && i < blk1 && sp.base + i * TK < w_hi && sp.base + i * TK > w_lo - TK; };
 
     // Step c of this split works on block blk0 + c. Before its barrier: its K, V and scales, places of it and the next.
     if (wave == 0) {
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
             for (int j = 0; j < F::NQH; ++j) vsq[j] = *reinterpret_cast<const f32x4 *>(vs_at + 4 * NG * j);
             __builtin_amdgcn_sched_barrier(0);
             float big = big_all;
-            const bool edge = mask != all || t0 < w_lo_max || t0 + TK > w_hi_min;
+            const bool edge = mask != all || t0 < w_lo_max || t0 > w_hi_min - TK;
             // the lane's row sees key 4 g + k of the part: bit k
             const uint64_t sees = seen_bits(mask >> (4 * g), row_lo - t0 - 4 * g, row_hi - t0 - 4 * g) >> (h * (TK / F::HV));
             if (edge) { // a key that a row does not see scores -inf there
@@ -530,8 +530,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tiled_kernel(const AttnArgs a
     if constexpr (KIND == WQ_KV_F16) {
         // Codes that are not finite and were taken out: what sees one is not finite either, whatever else it sums. Here
         // and not in the step, where this loop's registers would add to all the others (8 spilled, 52 with two parts).
-        const int last = min(sp.base + bad_to * TK, w_hi);
-        for (int pos = max(sp.base + bad_from * TK, w_lo); bad_from < bad_to && pos < last; ++pos) {
+        const int last = (int)min((long)sp.base + (long)bad_to * TK, (long)w_hi);
+        for (int pos = max(position(sp.base, bad_from, TK, 0), w_lo); bad_from < bad_to && pos < last; ++pos) {
             const int idx = page_index(a.c, pos), page = table[idx], slot = pos - idx * a.c.page;
             if (page < 0 || page >= a.c.pages) continue;
             const f16 *src = (const f16 *)(vp + ((OFF)page * (OFF)a.c.rp + (OFF)slot * (OFF)a.c.rs));

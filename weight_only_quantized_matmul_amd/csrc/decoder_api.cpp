@@ -304,7 +304,7 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
     if (!float_type(dtype) || H <= 0 || H % cache->heads != 0 || q_tok < 0 || q_head < 0 || o_tok < 0 || o_head < 0 ||
         window < 0 || !std::isfinite(scale))
         return WQ_E_INVAL;
-    if (H > WQ_KV_MAX_HEADS) return WQ_E_UNSUPPORTED;
+    if (H > WQ_KV_MAX_HEADS || (long)batch->T * (H / cache->heads) > (long)INT_MAX) return WQ_E_UNSUPPORTED;
     if (batch->T == 0) return WQ_OK;
     const int size = size_of(dtype);
     if (q == nullptr || o == nullptr || !aligned(q, size) || !aligned(o, size) || !aligned(lse, 4)) return WQ_E_INVAL;

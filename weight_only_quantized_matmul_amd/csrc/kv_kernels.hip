@@ -69,7 +69,7 @@ __device__ __forceinline__ void locate(const KvCopyArgs &a, Where &w, int lane) 
         const int first = a.b.q_start[i], next = a.b.q_start[i + 1], kv = a.b.kv_len[i];
         if (first <= w.tok && w.tok < next) {
             seq = i;
-            t = kv - next + w.tok;
+            t = max(kv, 0) - next + w.tok;
         }
     }
     const int base = (threadIdx.x & 63) - lane;
