@@ -179,3 +179,25 @@ def test_negative_lengths_are_empty(kv):
     wq.wq_attn_paged_dev(cache, batch, q, o, scale=0.1, lse=l)
     assert all(torch.equal(a, b) for a, b in zip(was, cache.tensors))
     assert not back.any() and not o.any() and (l == -float("inf")).all()
+
+
+def test_numbers_past_a_c_int():
+    """A window longer than any position is no window; negative and too large counts are refused, not taken modulo 2^32."""
+    cache, batch, q, _ = far_context(1)
+    lens = torch.tensor([3000], dtype=torch.int32, device="cuda")
+    batch = wq.KvBatch(batch.tensors[0], lens, batch.tensors[2], 1, max_q=1 << 32, max_kv=(1 << 32) + 5)
+    want = torch.empty_like(q)
+    wq.wq_attn_paged_dev(cache, batch, q, want, scale=0.125)
+    for window in ((1 << 31) - 1, 1 << 31, (1 << 32) + 1, 1 << 63):
+        o = torch.empty_like(q)
+        wq.wq_attn_paged_dev(cache, batch, q, o, scale=0.125, window=window)
+        assert torch.equal(o, want), window
+    for window in (-1, -(1 << 32)):
+        with pytest.raises(wq.WqError) as e:
+            wq.wq_attn_paged_dev(cache, batch, q, want, scale=0.125, window=window)
+        assert e.value.code == wq.WQ_E_INVAL
+    with pytest.raises(ValueError):
+        wq.KvBatch(batch.tensors[0], lens, batch.tensors[2], (1 << 32) + 1)
+    x = torch.ones((1, 4), device="cuda").expand((1 << 32) + 1, 4)
+    with pytest.raises(ValueError):
+        wq.wq_rmsnorm_dev(x, torch.ones(4, device="cuda"), 1e-6, x)

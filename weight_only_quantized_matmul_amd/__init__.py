@@ -413,6 +413,15 @@ _OUTS = {} if torch is None else {torch.int8: WQ_DT_I8, **_FLOATS}
 # in one condition, and the message is made only when it fails.
 
 
+_INT_MAX = 0x7FFFFFFF
+
+
+def _int(v):
+    """v for a C int, which ctypes would take modulo 2^32: larger numbers become the largest one, smaller ones -1."""
+    v = int(v)
+    return v if -1 <= v <= _INT_MAX else _INT_MAX if v > 0 else -1
+
+
 def _raw_stream(stream, dev):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -425,7 +434,7 @@ def _first(t, dims, types, what):
         raise TypeError("%s must be a torch tensor on a GPU" % what)
     dt = types.get(t.dtype, -1)
     shape, st, dev = t.shape, t.stride(), t.get_device()
-    if dt < 0 or dev < 0 or len(shape) != dims or (st[-1] != 1 and shape[-1] > 1):
+    if dt < 0 or dev < 0 or len(shape) != dims or (st[-1] != 1 and shape[-1] > 1) or max(shape) > _INT_MAX:
         raise ValueError("%s: a %s tensor of shape %s and strides %s on %s is not taken" % (what, t.dtype, tuple(shape), st, t.device))
     return shape, dt, dev, st
 
@@ -484,9 +493,9 @@ def wq_rope_create(rot: int, pairing: int, theta: float, sections) -> Rope:
 
     pairing 0 pairs element i with i + rot/2, pairing 1 element 2i with 2i + 1."""
     sec = list(sections)
-    arr = (ctypes.c_int * max(1, len(sec)))(*sec)
+    arr = (ctypes.c_int * max(1, len(sec)))(*map(_int, sec))
     h = ctypes.c_void_p(None)
-    _check(lib.wq_rope_create(int(rot), int(pairing), float(theta), arr, len(sec), ctypes.byref(h)), "wq_rope_create")
+    _check(lib.wq_rope_create(_int(rot), _int(pairing), float(theta), arr, len(sec), ctypes.byref(h)), "wq_rope_create")
     return Rope(h, int(rot), len(sec))
 
 
@@ -554,9 +563,11 @@ class KvBatch:
         B, width = table.shape
         if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
             raise ValueError("q_start, kv_len and table must hold B + 1, B and B rows")
-        self.B, self.T, self.device, self.dev = B, int(T), q_start.device, q_start.get_device()
+        if max(B, width, int(T)) > _INT_MAX:
+            raise ValueError("a batch of %d sequences, %d pages each and %d tokens is not taken" % (B, width, int(T)))
+        self.B, self.T, self.device, self.dev = B, _int(T), q_start.device, q_start.get_device()
         self.tensors = (q_start, kv_len, table)
-        self.c = _KvBatchC(B, self.T, width, int(max_q), int(max_kv), table.stride(0), q_start.data_ptr(),
+        self.c = _KvBatchC(B, self.T, width, _int(max_q), _int(max_kv), table.stride(0), q_start.data_ptr(),
                            kv_len.data_ptr(), table.data_ptr())
         self.ref = ctypes.byref(self.c)
 
@@ -602,7 +613,7 @@ def wq_attn_paged_dev(cache: KvCache, batch: KvBatch, q, o, scale: float, causal
         if _more(lse, shape[:2], torch.float32, dev, "lse")[0] != H and T > 1:
             raise ValueError("lse must be contiguous")
         lp = lse.data_ptr()
-    rc = lib.wq_attn_paged_dev(cache.ref, batch.ref, q.data_ptr(), dt, H, qs[0], qs[1], scale, 1 if causal else 0, window,
+    rc = lib.wq_attn_paged_dev(cache.ref, batch.ref, q.data_ptr(), dt, H, qs[0], qs[1], scale, 1 if causal else 0, _int(window),
                                o.data_ptr(), os_[0], os_[1], lp, _raw_stream(stream, dev))
     if rc:
         _check(rc, "wq_attn_paged_dev")
