@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():  # pragma: no cover - CPU hosts
     pytest.skip("no GPU", allow_module_level=True)
 
+import decoder_ref as ref  # noqa: E402
 import gpu_util as gu  # noqa: E402
 import weight_only_quantized_matmul_amd as wq  # noqa: E402
 
@@ -102,3 +103,24 @@ def test_norm_infinities_behind_zero_weights(rows, n, bad):
     wq.wq_rmsnorm_dev(x, w, 1e-6, y, y_scale=sc)
     assert sc[rows - 1].isnan() and not y[rows - 1].any()
     assert (y[:-1, : n // 2] == 127).all() and (y[:-1, n // 2] == 0).all() and (sc[:-1] > 0).all()
+
+
+@pytest.mark.parametrize("pairing", [0, 1])
+@pytest.mark.parametrize("theta,rot,sections", [(1e4, 128, [64]), (1e6, 64, [16, 16]), (3.0, 8, [4])])
+def test_rope_of_far_positions(pairing, theta, rot, sections):
+    """Every int32 position: within 8 u (|a| + |b|) + u |y|, the bound for near ones. The reference's angles, in 80 bits,
+    are within 2^31 * 2^-64 * 2 turns."""
+    rng = np.random.default_rng(rot)
+    T = 400
+    x = torch.from_numpy(rng.normal(size=(T, 2, rot)).astype(np.float32)).cuda()
+    pos = rng.integers(-(1 << 31), 1 << 31, (len(sections), T)).astype(np.int32)
+    pos[:, :4] = [(1 << 31) - 1, -(1 << 31), (1 << 24) + 1, 0]
+    y = torch.empty_like(x)
+    wq.wq_rope_dev(wq.wq_rope_create(rot, pairing, theta, sections), x, torch.from_numpy(pos).cuda(), y)
+    x64 = f64(x)
+    want = ref.rope(x64, pos, rot, pairing, theta, sections)
+    i = np.arange(rot // 2)
+    a, b = (i, i + rot // 2) if pairing == 0 else (2 * i, 2 * i + 1)
+    mag = np.zeros_like(x64)
+    mag[..., a] = mag[..., b] = np.abs(x64[..., a]) + np.abs(x64[..., b])
+    assert (np.abs(f64(y) - want) <= 8 * U * mag + 1.01 * U * np.abs(want)).all()
