@@ -494,6 +494,18 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
                       long q_head, float scale, int causal, int window, void *o, long o_tok, long o_head, float *lse,
                       void *hip_stream);
 
+/*
+ * The plan of wq_attn_paged_dev for these sizes as text (host only; buffers
+ * are not looked at, 256 CUs where the device is not open), for tests and
+ * logs: "few rows=16 step=32 splits=12 least=8 join=4x8 workspace=...", or
+ * "tiled waves=8 rows=256 ...": the kernel, rows a tile, positions a step, the
+ * most splits of a tile's positions and the fewest steps a split takes, how
+ * the join reads them (waves a row x partial rows in flight, 0x0: no splits)
+ * and the workspace in bytes.
+ */
+int wq_describe_attn(const wq_kv_cache *cache, const wq_kv_batch *batch, int dtype, int H, int causal, int window, char *buf,
+                     size_t buflen);
+
 #ifdef __cplusplus
 }
 #endif

@@ -100,6 +100,7 @@ def _bind(lib):
         "wq_rope_free": (ci, [vp]),
         "wq_kv_append_dev": (ci, [cachep, batchp, vp, vp, ci, cl, cl, vp]),
         "wq_kv_read_dev": (ci, [cachep, batchp, vp, vp, ci, cl, cl, vp]),
+        "wq_describe_attn": (ci, [cachep, batchp, ci, ci, ci, ci, ctypes.c_char_p, ctypes.c_size_t]),
         "wq_attn_paged_dev": (ci, [cachep, batchp, vp, ci, ci, cl, cl, cf, ci, ci, vp, cl, cl, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -617,3 +618,10 @@ def wq_attn_paged_dev(cache: KvCache, batch: KvBatch, q, o, scale: float, causal
                                o.data_ptr(), os_[0], os_[1], lp, _raw_stream(stream, dev))
     if rc:
         _check(rc, "wq_attn_paged_dev")
+
+
+def wq_describe_attn(cache, batch, dtype: int, H: int, causal: bool = True, window: int = 0) -> str:
+    """The plan of wq_attn_paged_dev for queries of H heads and type code dtype (WQ_DT_F32, ...)."""
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.wq_describe_attn(cache.ref, batch.ref, dtype, H, 1 if causal else 0, _int(window), buf, len(buf)), "wq_describe_attn")
+    return buf.value.decode()

@@ -296,6 +296,16 @@ struct AttnPlan {
     size_t ws_bytes;
 };
 
+// How the join reads `rows` rows of nsplit splits: one wave a row once that gives every CU four rows and there are few
+// splits, else four; enough partial rows in flight for all splits, at most eight a wave.
+struct JoinPlan {
+    int waves, at;
+};
+inline JoinPlan plan_join(long rows, int nsplit) {
+    if (rows >= 1024 && nsplit <= 16) return {1, 4};
+    return {4, nsplit <= 8 ? 2 : 8};
+}
+
 // Partial results of a split: row (token, head) and split s at part[(row * nsplit + s) * D], the exponent they
 // are scaled by (2^-ref) and their sum of probabilities at ml[(row * nsplit + s) * 2].
 struct Partials {

@@ -114,10 +114,10 @@ hipError_t launch_d(const AttnArgs &a, const AttnPlan &p, const Partials &pt, hi
     const long rows = (long)a.b.T * a.H;
     if (rows > kMaxThreads / 256) return hipErrorNotSupported;
     const dim3 block(256);
-    // enough partial rows in flight for all splits, at most eight a wave
-    if (rows >= 1024 && pt.nsplit <= 16)
+    const JoinPlan j = plan_join(rows, pt.nsplit);
+    if (j.waves == 1)
         hipLaunchKernelGGL((attn_join_kernel<T, D, 4, 1>), dim3((unsigned)((rows + 3) / 4)), block, 0, st, a, pt, p.rows, p.step);
-    else if (pt.nsplit <= 8)
+    else if (j.at == 2)
         hipLaunchKernelGGL((attn_join_kernel<T, D, 2, 4>), dim3((unsigned)rows), block, 0, st, a, pt, p.rows, p.step);
     else
         hipLaunchKernelGGL((attn_join_kernel<T, D, 8, 4>), dim3((unsigned)rows), block, 0, st, a, pt, p.rows, p.step);

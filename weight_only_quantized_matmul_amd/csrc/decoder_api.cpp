@@ -2,6 +2,7 @@
 // (include/wqmm.h): argument checks and launches.
 #include <climits>
 #include <cmath>
+#include <cstdio>
 #include <new>
 
 #include "attn_common.h"
@@ -346,6 +347,27 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
                          : wq::launch_attn_tiled(a, p, pt, cache->kind, cache->dim, dtype, vec, wide, (hipStream_t)hip_stream);
     if (e == hipSuccess && p.nsplit > 1) e = wq::launch_attn_join(a, p, pt, cache->dim, dtype, (hipStream_t)hip_stream);
     return status(e);
+}
+
+int wq_describe_attn(const wq_kv_cache *cache, const wq_kv_batch *batch, int dtype, int H, int causal, int window, char *buf,
+                     size_t buflen) {
+    int rc = check_cache(cache);
+    if (rc == WQ_OK) rc = check_batch(batch);
+    if (rc != WQ_OK) return rc;
+    if (!float_type(dtype) || H <= 0 || H % cache->heads != 0 || window < 0 || buf == nullptr || buflen == 0) return WQ_E_INVAL;
+    if (batch->T == 0) {
+        snprintf(buf, buflen, "none");
+        return WQ_OK;
+    }
+    const bool open = cache->device >= 0 && cache->device < WQ_MAX_DEVICES && wq::device_cus(cache->device) > 0;
+    const wq::AttnPlan p =
+        plan_attn(cache, batch, H, causal != 0, window, dtype == WQ_DT_F32, open ? wq::device_cus(cache->device) : 256);
+    const wq::JoinPlan j = wq::plan_join((long)batch->T * H, p.nsplit);
+    char kernel[32];
+    snprintf(kernel, sizeof kernel, p.few ? "few" : "tiled waves=%d", p.waves);
+    snprintf(buf, buflen, "%s rows=%d step=%d splits=%d least=%d join=%dx%d workspace=%zu", kernel, p.rows, p.step, p.nsplit, p.least,
+             p.nsplit > 1 ? j.waves : 0, p.nsplit > 1 ? j.at : 0, p.ws_bytes);
+    return WQ_OK;
 }
 
 } // extern "C"
