@@ -25,8 +25,9 @@
 //
 // Next to the bytes the opening of codes is what costs: K's and V's of a step
 // are about 370 of its 850 vector instructions in int4. 64 ragged sequences up to
-// 8192 positions (48 heads over 8, int8, 672 MB) take 138 us (4.9 TB/s); four of
-// 131072 in int4 (571 MB) 137 us (4.2 TB/s, vector units 68 % busy); one of 1500 9 us.
+// 8192 positions (48 heads over 8, int8, 672 MB) take 139 us (4.8 TB/s); four of
+// 131072 in int4 (571 MB) 143 us (4.0 TB/s, vector units 69 % busy); one of 1500
+// 8 us (medians of the kernel alone, clocks settled).
 #include "attn_common.h"
 
 namespace wq {

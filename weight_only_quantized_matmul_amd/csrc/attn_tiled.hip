@@ -20,10 +20,11 @@
 // against 2.08e-4), so f16 queries take two parts: that prompt in 259 us.
 //
 // Bound by the vector units and the matrix units in turn (the softmax costs six
-// instructions and an exponential an element). 4096 tokens, causal, 32 heads over
-// 8, bf16 on an f16 cache: 137 GFLOP in 200 us (686 TFLOP/s); eight chunks of up
-// to 511 tokens on up to 5000 positions, f32 on int8: 159 GFLOP, 2.5 times that
-// in parts, in 456 us.
+// instructions and an exponential an element). With the clocks settled (after a
+// hundred passes; the first 20 after idling take a quarter more): 4096 tokens,
+// causal, 32 heads over 8, bf16 on an f16 cache, 137 GFLOP in 202 us
+// (680 TFLOP/s); eight chunks of up to 511 tokens on up to 5000 positions, f32 on
+// int8, 159 GFLOP, 2.5 times that in parts, in 450 us.
 #include "attn_common.h"
 
 namespace wq {
@@ -53,7 +54,9 @@ struct Mma<16> {
 template <typename T, int KIND, int D, int NW>
 struct Tiled {
     static constexpr int RW = tiled_rows(D, sizeof(T) == 4); // rows a wave
-    static constexpr int TK = D == 256 ? 32 : 64;    // positions a step (LDS: 4 buffers of TK * D halves, two blocks a CU)
+    // Positions a step. LDS holds 4 buffers of TK * D halves, 75 KiB for rows of 128 and 256: two four-wave blocks a CU. Of
+    // eight waves a CU holds one block, whose 164 to 241 registers leave two waves a SIMD.
+    static constexpr int TK = D == 256 ? 32 : 64;
     static constexpr int NT = 64 * NW, R = RW * NW;
     static constexpr int NG = 64 / RW;               // lanes that share a row
     static constexpr int CH = D / 8, CV = TK / 8;    // 16-byte chunks of a K row and of a V^T row in LDS

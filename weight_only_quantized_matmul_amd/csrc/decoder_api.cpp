@@ -128,8 +128,10 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     if (window > 0 && causal && (long)window + q < kv) kv = (long)window + q;
     const int row = c->kind == WQ_KV_F16 ? 2 * c->dim : c->kind == WQ_KV_I8 ? c->dim : c->dim / 2;
     // Up to 64 rows (32 of 256 elements) the few-rows kernel reads the cache once a tile of 32 (16) rows, the second
-    // time from L2, and still beats tiles of which half the rows are empty (60 rows on 19531 positions: 38 us, tiled 70;
-    // on 38 positions 14.6 and 13.6).
+    // time from L2, and on contexts of a thousand positions beats tiles of which half the rows are empty (60 rows of 128,
+    // f32 on int8, 1000 positions: 15 us with one key/value head, tiled 19; 16.5 and 19.7 with eight). On long ones it
+    // still does for rows of 64 and for int4 with one head (19531 positions: 14.5 and 20.6, 19.3 and 22.0) but not with
+    // eight heads (43 and 31 us).
     p.few = q * G <= (c->dim <= 128 ? 64 : 32);
     p.waves = 4;
     if (p.few) {
@@ -137,8 +139,8 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
         p.step = row <= 64 ? 64 : 32;
     } else {
         // Eight waves share each opened tile where opening is dear (rows of 128 and 256) and their larger tiles still
-        // give every CU a block: prefill of 4096 tokens 216 us, with four waves 268. Rows of 64 do better with more,
-        // smaller blocks (13 prompts of up to 1695 tokens, window 507: four waves 43 us, eight 91).
+        // give every CU a block: prefill of 4096 tokens 202 us, with four waves 232. Rows of 64 do better with more,
+        // smaller blocks (13 prompts of up to 1695 tokens, window 507: four waves 43 us, eight 91 when they were there).
         const long wave_rows = wq::tiled_rows(c->dim, f32);
         if (c->dim > 64 && (q * G + 8 * wave_rows - 1) / (8 * wave_rows) * b->B * c->heads >= cus) p.waves = 8;
         p.rows = (int)wave_rows * p.waves;
@@ -150,8 +152,8 @@ wq::AttnPlan plan_attn(const wq_kv_cache *c, const wq_kv_batch *b, int H, int ca
     const long total = (tiles < numbers ? tiles : numbers) * c->heads * steps;
     if (p.few) {
         long per_wave = total / (cus * 12);
-        // many sequences differ in length: shorter splits even that out (64 ragged sequences: 150 us with 512 positions
-        // a wave, 155 with 1024); few are split for the chip's sake and pay for each split's start (4 long ones: 179 and 154 us)
+        // many sequences differ in length: shorter splits even that out (64 ragged sequences: 147 us with 512 positions
+        // a wave, 173 with 1024); few are split for the chip's sake and pay for each split's start (4 long ones: 146 and 143 us)
         const long most = ((tiles < numbers ? tiles : numbers) * c->heads >= cus ? 512 : 1024) / p.step;
         per_wave = per_wave < 1 ? 1 : per_wave > most ? most : per_wave;
         p.least = (int)(4 * per_wave);

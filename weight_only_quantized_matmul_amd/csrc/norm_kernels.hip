@@ -9,7 +9,8 @@
 // Bound by HBM at many rows: 8191 x 6144, bf16 and residual in, sum and int8
 // out, 352 MB in 77 us (4.6 TB/s; a device copy reaches 5.46). A block there
 // walks rows (one row a block, w read again for each: 94 us). One row of 6144
-// in f32 takes 3.6 us, latency.
+// in f32 takes 3.4 us, latency. Rows that leave fp32's range when squared pay a
+// second reduction.
 #include "decoder.h"
 
 namespace wq {
@@ -227,9 +228,9 @@ template <typename TX, typename TY, int VEC, bool ANY>
 hipError_t launch_nv(const NormArgs &a, int cus, hipStream_t st) {
     const int chunks = (a.n + VEC - 1) / VEC;
     // With rows for every CU, the smallest block whose threads hold at most four
-    // loads (several blocks a CU; with eight, 6144 fp32 elements to int8 spill: 331
-    // against 127 us for 8138 rows); with few rows, up to 1024 threads: the latency
-    // of one row is what counts then.
+    // loads (several blocks a CU; with eight, the row-walking form of 6144 fp32
+    // elements to int8 spilled: 331 us for 8138 rows, now 118); with few rows, up to
+    // 1024 threads: the latency of one row is what counts then.
     constexpr int LAST = 32768 / 1024 / VEC; // loads a thread at the longest row
     int nv = 0;
     for (int want = a.rows >= 2 * cus ? 256 : 1024; want <= 1024 && nv == 0; want *= 2)
