@@ -387,6 +387,26 @@ int wq_rmsnorm_dev(int device, const void *x, int x_dtype, long x_stride, const 
                    void *sum_out, long sum_stride, void *hip_stream);
 
 /*
+ * The norms around a block's output x, with its gate and the residual between them:
+ *     z = x / sqrt(mean(x^2) + eps) * w_post      (w_post NULL: z = x)
+ *     r = residual + alpha * gate * z             (gate NULL: 1)
+ *     y = r / sqrt(mean(r^2) + eps) * w_pre
+ * x, gate, residual, sum_out: [rows, n] of x_dtype (f32, bf16, f16) with row
+ * strides x_stride, gate_stride (0: one row of gates for all), res_stride,
+ * sum_stride; w_post, w_pre: n floats; y: [rows, n] of y_dtype (f32, bf16,
+ * f16), row stride y_stride. sum_out (NULL: not kept) receives r rounded to
+ * x_dtype; the second norm is taken of the unrounded r. y and w_pre may both be
+ * NULL (only sum_out is written). Everything between is fp32; finite rows of
+ * any size have finite squares (a row of zeros with eps 0 is 0 / 0, a NaN).
+ * sum_out may be x, gate or residual (same stride, and rows that no other row
+ * reads), and so may y when the types agree too, but not the one that is
+ * sum_out. n <= WQ_NORM_MAX_N (WQ_E_UNSUPPORTED above); rows == 0 is a no-op.
+ */
+int wq_rmsnorm_block_dev(int device, const void *x, int x_dtype, long x_stride, const float *w_post, const void *gate,
+                         long gate_stride, float alpha, const void *residual, long res_stride, const float *w_pre, float eps,
+                         int rows, int n, void *y, int y_dtype, long y_stride, void *sum_out, long sum_stride, void *hip_stream);
+
+/*
  * Rotary positions. The first `rot` elements of a head (even, at most
  * WQ_ROPE_MAX_ROT) form rot/2 pairs; pair i is (x[i], x[i + rot/2]) with
  * pairing 0 and (x[2i], x[2i+1]) with pairing 1, and is turned by the angle
@@ -461,6 +481,20 @@ typedef struct wq_kv_batch {
 int wq_kv_append_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const void *k_new, const void *v_new,
                      int dtype, long tok, long head, void *hip_stream);
 
+/*
+ * Rotary positions and append in one launch: the queries q [T, H, dim] of dtype
+ * are turned into q_out (NULL, both: none; q_out may be q with q's strides), the
+ * keys k_new are turned, rounded to fp32 and quantised into their slots as by
+ * wq_kv_append_dev, the values v_new as they are. Turning follows wq_rope_dev
+ * with the plan `rope` (rot <= dim), in fp64 up to that rounding. pos: device
+ * int32 [axes, T], row stride pos_stride; NULL (plans of one axis only): each
+ * token's position p in its sequence. Tokens that have no place in the cache
+ * are turned all the same; rows past q_start[B] are left as they were.
+ */
+int wq_kv_append_rope_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const wq_rope *rope, const void *q, int H,
+                          long q_tok, long q_head, void *q_out, long qo_tok, long qo_head, const void *k_new, const void *v_new,
+                          int dtype, long tok, long head, const int *pos_dev, long pos_stride, void *hip_stream);
+
 /* The values the batch's T tokens have in the cache, code * scale in fp32
  * rounded to dtype, as k_out, v_out [T, heads, dim] with strides tok, head. */
 int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_out, void *v_out, int dtype, long tok,
@@ -505,6 +539,71 @@ int wq_attn_paged_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const 
  */
 int wq_describe_attn(const wq_kv_cache *cache, const wq_kv_batch *batch, int dtype, int H, int causal, int window, char *buf,
                      size_t buflen);
+
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer without the host in between: the choice of each
+ * token's experts, and the experts' gated feed-forward over tokens whose
+ * experts only the device knows. Stream-ordered and capturable like the calls
+ * above.
+ */
+#define WQ_MOE_MAX_EXPERTS 1024
+#define WQ_MOE_MAX_GROUPS 64
+#define WQ_MOE_MAX_K 32
+#define WQ_MOE_MAX_ROWS 16384 /* most T * k of wq_moe_ffn_dev */
+
+enum wq_gating { WQ_GATE_SOFTMAX = 0, WQ_GATE_SIGMOID = 1 };
+
+/*
+ * The k experts of each of T tokens, from the router's scores [T, E] of dtype
+ * (f32, bf16, f16; row stride `stride`):
+ *     p = softmax over the E scores, or sigmoid of each;   c = p + bias
+ * (bias: E floats; NULL: c = p). The experts stand in `groups` groups of
+ * E / groups; a group's value is the sum of its two largest c (of its one,
+ * where it has one), and only the top_groups groups of largest value are left.
+ * ids [T, k] (int32, contiguous) receives the k experts of largest c among
+ * them, in descending order; weights [T, k] (floats, contiguous) their p,
+ * divided by the sum of the k if `normalise`, times scale. Of equal values the
+ * lower index goes first. p, c and sums are fp64. A NaN score counts as -inf,
+ * +inf as the largest fp32; where softmax sees -inf only, every p is 0; a sum of
+ * 0 leaves weights of 0. A NaN c counts as -inf.
+ * 1 <= k <= E / groups * top_groups. WQ_E_UNSUPPORTED: E > WQ_MOE_MAX_EXPERTS,
+ * groups > WQ_MOE_MAX_GROUPS, k > WQ_MOE_MAX_K. T == 0 is a no-op.
+ */
+int wq_moe_route_dev(int device, const void *scores, int dtype, int T, int E, long stride, const float *bias, int gating,
+                     int groups, int top_groups, int k, int normalise, float scale, int *ids, float *weights,
+                     void *hip_stream);
+
+/*
+ * The layer's E experts: host arrays of resident tensors on one device, all in
+ * one quantized format (WQ_F32: WQ_E_UNSUPPORTED), gate[e] and up[e] all of one
+ * shape [F, D] and group size, down[e] all of one shape [D_out, F] and group size
+ * (else WQ_E_INVAL). A tensor may stand in several places. The layer
+ * references the tensors: free it before them. Tensors of 4 GiB and more:
+ * WQ_E_UNSUPPORTED.
+ */
+typedef struct wq_moe wq_moe;
+int wq_moe_create(wq_tensor *const *gate, wq_tensor *const *up, wq_tensor *const *down, int E, wq_moe **moe);
+int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
+
+/*
+ * The layer for a few tokens:
+ *     y[t] = add[t] + sum_j weights[t,j] * down_e . h,   e = ids[t,j],
+ *     h = silu(gate_e . x[t]) * (up_e . x[t]),           silu(z) = z / (1 + e^-z)
+ * x [T, D], add (NULL: zeros) and y [T, D_out] of dtype (f32, bf16, f16) with
+ * row strides x_stride, add_stride, y_stride; ids int32 [T, k] and weights float
+ * [T, k] contiguous on the device. An id outside [0, E) adds nothing (a place
+ * of a batch without a token, an expert that lives elsewhere); an expert that
+ * stands twice counts twice. y may be x or add (same stride).
+ * The products are exact in their operands as in wq_matmul_dev (16-bit
+ * activations enter as they are, h in full fp32); sums are fp32, the sum over
+ * j in the order of j, y rounded once. A token's result does not depend on the
+ * other tokens. It uses the stream's workspace as wq_matmul_dev's tiled path
+ * does (it may grow, but not while the stream is being captured).
+ * For many tokens an expert the grouped calls are faster; T * k above
+ * WQ_MOE_MAX_ROWS gives WQ_E_UNSUPPORTED. T == 0 is a no-op.
+ */
+int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
+                   int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream);
 
 #ifdef __cplusplus
 }

@@ -37,6 +37,8 @@ WQ_E_FAULT = -7
 WQ_E_UNSUPPORTED = -8
 WQ_DT_F32, WQ_DT_BF16, WQ_DT_F16, WQ_DT_I8 = 0, 1, 2, 3
 WQ_KV_F16, WQ_KV_I8, WQ_KV_I4 = 0, 1, 2
+WQ_GATE_SOFTMAX, WQ_GATE_SIGMOID = 0, 1
+WQ_MOE_MAX_EXPERTS, WQ_MOE_MAX_GROUPS, WQ_MOE_MAX_K, WQ_MOE_MAX_ROWS = 1024, 64, 32, 16384
 WQ_NORM_MAX_N = 32768
 WQ_ROPE_MAX_ROT = 256
 WQ_ROPE_MAX_AXES = 8
@@ -95,6 +97,12 @@ def _bind(lib):
         "wq_matmul_dev_noalloc": (ci, [vp, vp, ci, vp, vp]),
         "wq_noalloc_scratch_bytes": (ctypes.c_size_t, []),
         "wq_rmsnorm_dev": (ci, [ci, vp, ci, cl, vp, cl, vp, cf, ci, ci, vp, ci, cl, vp, vp, cl, vp]),
+        "wq_rmsnorm_block_dev": (ci, [ci, vp, ci, cl, vp, vp, cl, cf, vp, cl, vp, cf, ci, ci, vp, ci, cl, vp, cl, vp]),
+        "wq_kv_append_rope_dev": (ci, [cachep, batchp, vp, vp, ci, cl, cl, vp, cl, cl, vp, vp, ci, cl, cl, vp, cl, vp]),
+        "wq_moe_route_dev": (ci, [ci, vp, ci, ci, ci, cl, vp, ci, ci, ci, ci, ci, cf, vp, vp, vp]),
+        "wq_moe_create": (ci, [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp), ci, ctypes.POINTER(vp)]),
+        "wq_moe_free": (ci, [vp]),
+        "wq_moe_ffn_dev": (ci, [vp, vp, ci, ci, cl, vp, vp, ci, vp, cl, vp, cl, vp]),
         "wq_rope_create": (ci, [ci, ci, ctypes.c_double, _c_int_p, ci, ctypes.POINTER(vp)]),
         "wq_rope_dev": (ci, [vp, ci, vp, ci, ci, ci, ci, cl, cl, vp, cl, vp, cl, cl, vp]),
         "wq_rope_free": (ci, [vp]),
@@ -477,6 +485,40 @@ def wq_rmsnorm_dev(x, w, eps: float, y, residual=None, sum_out=None, y_scale=Non
         _check(rc, "wq_rmsnorm_dev")
 
 
+def wq_rmsnorm_block_dev(x, residual, eps: float, w_post=None, gate=None, alpha: float = 1.0, w_pre=None, y=None, sum_out=None,
+                         stream=None) -> None:
+    """Norm of a block's output x[rows, n] times w_post, times gate and alpha, added to residual (sum_out), and its norm
+    times w_pre (y). gate has x's type and shape, or one row for all."""
+    shape, dt, dev, xs = _first(x, 2, _FLOATS, "x")
+    rows, n = shape
+    rs = _more(residual, shape, x.dtype, dev, "residual")
+    gp = pp = wp = yp = sp = None
+    gs = ys = ss = ydt = 0
+    if w_post is not None:
+        _more(w_post, shape[1:], torch.float32, dev, "w_post")
+        pp = w_post.data_ptr()
+    if gate is not None:
+        if gate.shape[0] == 1 and rows != 1:
+            _more(gate, torch.Size((1, n)), x.dtype, dev, "gate")
+        else:
+            gs = _more(gate, shape, x.dtype, dev, "gate")[0]
+        gp = gate.data_ptr()
+    if (y is None) != (w_pre is None):
+        raise ValueError("y goes with w_pre")
+    if y is not None:
+        ydt = _FLOATS.get(y.dtype, -1)
+        ys = _more(y, shape, y.dtype, dev, "y")[0]
+        _more(w_pre, shape[1:], torch.float32, dev, "w_pre")
+        yp, wp = y.data_ptr(), w_pre.data_ptr()
+    if sum_out is not None:
+        ss = _more(sum_out, shape, x.dtype, dev, "sum_out")[0]
+        sp = sum_out.data_ptr()
+    rc = lib.wq_rmsnorm_block_dev(dev, x.data_ptr(), dt, xs[0], pp, gp, gs, alpha, residual.data_ptr(), rs[0], wp, eps, rows, n,
+                                  yp, ydt, ys, sp, ss, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_rmsnorm_block_dev")
+
+
 class Rope:
     """Plan of rotary positions (the C wq_rope*; host memory, released with the object or wq_rope_free)."""
 
@@ -592,6 +634,33 @@ def wq_kv_append_dev(cache: KvCache, batch: KvBatch, k_new, v_new, stream=None) 
         _check(rc, "wq_kv_append_dev")
 
 
+def wq_kv_append_rope_dev(cache: KvCache, batch: KvBatch, rope: Rope, k_new, v_new, q=None, q_out=None, pos=None, stream=None) -> None:
+    """Append with rotary positions: q_out[T, H, D] = q turned, keys turned and quantised, values quantised.
+
+    pos int32 [axes, T], or None for the tokens' positions in their sequences (one axis). q_out may be q."""
+    dt, st = _tokens(cache, batch, k_new, v_new, "k_new and v_new")
+    qp = op = pp = None
+    H = 0
+    qs = os_ = (0, 0)
+    ps = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q goes with q_out")
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != batch.T or q.shape[2] != cache.dim:
+            raise ValueError("q must have shape [%d, H, %d]" % (batch.T, cache.dim))
+        H = q.shape[1]
+        qs = _more(q, q.shape, k_new.dtype, cache.dev, "q")
+        os_ = _more(q_out, q.shape, k_new.dtype, cache.dev, "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if pos is not None:
+        ps = _more(pos, torch.Size((rope.axes, batch.T)), torch.int32, cache.dev, "pos")[0]
+        pp = pos.data_ptr()
+    rc = lib.wq_kv_append_rope_dev(cache.ref, batch.ref, rope.ptr, qp, H, qs[0], qs[1], op, os_[0], os_[1], k_new.data_ptr(),
+                                   v_new.data_ptr(), dt, st[0], st[1], pp, ps, _raw_stream(stream, cache.dev))
+    if rc:
+        _check(rc, "wq_kv_append_rope_dev")
+
+
 def wq_kv_read_dev(cache: KvCache, batch: KvBatch, k_out, v_out, stream=None) -> None:
     """The values of the batch's tokens in the cache, into k_out, v_out [T, heads, D]."""
     dt, st = _tokens(cache, batch, k_out, v_out, "k_out and v_out")
@@ -625,3 +694,76 @@ def wq_describe_attn(cache, batch, dtype: int, H: int, causal: bool = True, wind
     buf = ctypes.create_string_buffer(256)
     _check(lib.wq_describe_attn(cache.ref, batch.ref, dtype, H, 1 if causal else 0, _int(window), buf, len(buf)), "wq_describe_attn")
     return buf.value.decode()
+
+
+# ----------------------------------------------------------------------------
+# Mixture of experts
+
+
+def wq_moe_route_dev(scores, ids, weights, bias=None, gating: int = WQ_GATE_SOFTMAX, groups: int = 1, top_groups: int = 1,
+                     normalise: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The experts (ids int32 [T, k]) and weights (float32 [T, k]) of T tokens from scores [T, E]; bias float32 [E]."""
+    shape, dt, dev, st = _first(scores, 2, _FLOATS, "scores")
+    T, E = shape
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    for t, dtype, what in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if _more(t, torch.Size((T, k)), dtype, dev, what)[0] != k and T > 1:
+            raise ValueError("%s must be contiguous" % what)
+    bp = None
+    if bias is not None:
+        _more(bias, shape[1:], torch.float32, dev, "bias")
+        bp = bias.data_ptr()
+    rc = lib.wq_moe_route_dev(dev, scores.data_ptr(), dt, T, E, st[0], bp, _int(gating), _int(groups), _int(top_groups), k,
+                              1 if normalise else 0, scale, ids.data_ptr(), weights.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_moe_route_dev")
+
+
+class Moe:
+    """Handle of a layer's experts (the C wq_moe*); it keeps their tensors' handles."""
+
+    def __init__(self, ptr: ctypes.c_void_p, gates, ups, downs):
+        self.ptr, self.tensors = ptr, (gates, ups, downs)
+        self.device, self.D, self.F, self.D_out = gates[0].device, gates[0].I, gates[0].O, downs[0].O
+
+
+def wq_moe_create(gates, ups, downs) -> Moe:
+    """The layer of experts gates[e], ups[e] [F, D] and downs[e] [D_out, F] (resident tensors, freed after it)."""
+    sets = [list(s) for s in (gates, ups, downs)]
+    E = len(sets[0])
+    if len(sets[1]) != E or len(sets[2]) != E:
+        raise ValueError("need a gate, an up and a down tensor per expert")
+    arrs = [(ctypes.c_void_p * max(1, E))(*[t.ptr.value for t in s]) for s in sets]
+    h = ctypes.c_void_p(None)
+    _check(lib.wq_moe_create(*arrs, E, ctypes.byref(h)), "wq_moe_create")
+    return Moe(h, *sets)
+
+
+def wq_moe_free(moe: Moe) -> None:
+    if moe is None:
+        return
+    _check(lib.wq_moe_free(moe.ptr), "wq_moe_free")
+    moe.ptr = ctypes.c_void_p(None)
+
+
+def wq_moe_ffn_dev(moe: Moe, x, ids, weights, y, add=None, stream=None) -> None:
+    """y[T, D_out] = add + the weighted sum of the feed-forward of x's [T, D] experts ids [T, k] (int32; others than the
+    layer's add nothing), weights float32 [T, k]."""
+    shape, dt, dev, xs = _first(x, 2, _FLOATS, "x")
+    T = shape[0]
+    if shape[1] != moe.D or dev != moe.device:
+        raise ValueError("x must have shape [T, %d] on GPU %d" % (moe.D, moe.device))
+    out = torch.Size((T, moe.D_out))
+    ys = _more(y, out, x.dtype, dev, "y")
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    for t, dtype, what in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if _more(t, torch.Size((T, k)), dtype, dev, what)[0] != k and T > 1:
+            raise ValueError("%s must be contiguous" % what)
+    ap, as_ = None, 0
+    if add is not None:
+        as_ = _more(add, out, x.dtype, dev, "add")[0]
+        ap = add.data_ptr()
+    rc = lib.wq_moe_ffn_dev(moe.ptr, x.data_ptr(), dt, T, xs[0], ids.data_ptr(), weights.data_ptr(), k, ap, as_, y.data_ptr(),
+                            ys[0], _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "wq_moe_ffn_dev")

@@ -24,6 +24,9 @@ namespace wq {
 int begin_call(int device);                                                    // WQ_OK, WQ_E_NOTINIT, WQ_E_FAULT
 int stream_workspace(int device, size_t bytes, hipStream_t st, void **out);    // the stream's workspace
 int device_cus(int device);
+bool device_is_open(int device);
+int device_table(int device, const void *host, size_t bytes, void **out); // a copy in the device's memory
+void device_table_free(int device, void *p, size_t bytes);
 
 // A dimension of a launch holds fewer than 2^32 threads; the runtime does not refuse more, it runs what is left of
 // their number modulo 2^32. Longer work is launched in pieces or laid over a second dimension, or refused
@@ -41,6 +44,16 @@ struct NormArgs {
     int rows, n;
 };
 hipError_t launch_rmsnorm(const NormArgs &a, int x_dtype, int y_dtype, bool vec, int cus, hipStream_t st);
+
+struct BlockNormArgs {
+    const void *x, *gate, *res;
+    const float *w_post, *w_pre;
+    void *y, *sum;
+    long xs, gs, rs, ys, ss;
+    float alpha, eps;
+    int rows, n;
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, int x_dtype, int y_dtype, bool vec, int cus, hipStream_t st);
 
 struct RopeArgs {
     const void *x;
@@ -80,6 +93,19 @@ struct KvCopyArgs {
 };
 hipError_t launch_kv_append(const KvCopyArgs &a, int kind, int dim, int dtype, bool vec, hipStream_t st);
 hipError_t launch_kv_read(const KvCopyArgs &a, int kind, int dim, int dtype, bool vec, hipStream_t st);
+
+struct KvRopeArgs {
+    KvView c;
+    BatchView b;
+    const void *q, *k, *v;
+    void *q_out;
+    const int *pos; // null: the tokens' positions in their sequences
+    long pos_stride, qt, qh, ot, oh, tok, head;
+    int H, rot, pairing;
+    double turns[WQ_ROPE_MAX_ROT / 2];
+    uint8_t axis[WQ_ROPE_MAX_ROT / 2];
+};
+hipError_t launch_kv_append_rope(const KvRopeArgs &a, int kind, int dim, int dtype, bool vec, int cus, hipStream_t st);
 
 struct AttnArgs {
     KvView c;

@@ -6,29 +6,9 @@
 #include <new>
 
 #include "attn_common.h"
+#include "entry.h"
 
 namespace {
-
-struct DeviceScope { // makes `dev` current, restoring the caller's device after
-    int prev = -1;
-    bool switched = false;
-    explicit DeviceScope(int dev) {
-        if (hipGetDevice(&prev) == hipSuccess && prev != dev) switched = hipSetDevice(dev) == hipSuccess;
-    }
-    ~DeviceScope() {
-        if (switched) (void)hipSetDevice(prev);
-    }
-};
-
-int status(hipError_t e) {
-    return e == hipSuccess ? WQ_OK : e == hipErrorOutOfMemory ? WQ_E_OOM : e == hipErrorNotSupported ? WQ_E_UNSUPPORTED : WQ_E_HIP;
-}
-
-bool float_type(int t) { return t >= WQ_DT_F32 && t <= WQ_DT_F16; }
-
-int size_of(int t) { return t == WQ_DT_F32 ? 4 : t == WQ_DT_I8 ? 1 : 2; }
-
-bool aligned(const void *p, long a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
 
 // A buffer whose rows start at multiples of `a` bytes (strides in elements of `size` bytes).
 bool rows_aligned(const void *p, long s0, long s1, int size, long a) {
@@ -216,6 +196,48 @@ int wq_rmsnorm_dev(int device, const void *x, int x_dtype, long x_stride, const 
     return status(wq::launch_rmsnorm(a, x_dtype, y_dtype, wide, wq::device_cus(device), (hipStream_t)hip_stream));
 }
 
+int wq_rmsnorm_block_dev(int device, const void *x, int x_dtype, long x_stride, const float *w_post, const void *gate,
+                         long gate_stride, float alpha, const void *residual, long res_stride, const float *w_pre, float eps,
+                         int rows, int n, void *y, int y_dtype, long y_stride, void *sum_out, long sum_stride, void *hip_stream) {
+    if (!float_type(x_dtype) || (y && !float_type(y_dtype))) return WQ_E_INVAL;
+    if (rows < 0 || n <= 0 || x_stride < 0 || res_stride < 0 || !(eps >= 0.f) || !std::isfinite(alpha)) return WQ_E_INVAL;
+    if ((gate && gate_stride < 0) || (y && y_stride < 0) || (sum_out && sum_stride < 0)) return WQ_E_INVAL;
+    if (n > WQ_NORM_MAX_N) return WQ_E_UNSUPPORTED;
+    if ((y == nullptr) != (w_pre == nullptr) || (y == nullptr && sum_out == nullptr)) return WQ_E_INVAL;
+    if (rows == 0) return WQ_OK;
+    if (x == nullptr || residual == nullptr) return WQ_E_INVAL;
+    const int sx = size_of(x_dtype), sy = y ? size_of(y_dtype) : 4;
+    if (!aligned(x, sx) || !aligned(residual, sx) || !aligned(gate, sx) || !aligned(sum_out, sx) || !aligned(y, sy) ||
+        !aligned(w_post, 4) || !aligned(w_pre, 4))
+        return WQ_E_INVAL;
+    const int rc = wq::begin_call(device);
+    if (rc != WQ_OK) return rc;
+    DeviceScope scope(device);
+    wq::BlockNormArgs a;
+    a.x = x;
+    a.gate = gate;
+    a.res = residual;
+    a.w_post = w_post;
+    a.w_pre = w_pre;
+    a.y = y;
+    a.sum = sum_out;
+    a.xs = x_stride;
+    a.gs = gate_stride;
+    a.rs = res_stride;
+    a.ys = y_stride;
+    a.ss = sum_stride;
+    a.alpha = alpha;
+    a.eps = eps;
+    a.rows = rows;
+    a.n = n;
+    const int vec = 16 / sx; // elements of a wide load of x
+    const long ya = vec * sy < 16 ? vec * sy : 16;
+    const bool wide = n % vec == 0 && rows_aligned(x, x_stride, 0, sx, 16) && rows_aligned(residual, res_stride, 0, sx, 16) &&
+                      aligned(w_post, 16) && aligned(w_pre, 16) && (!gate || rows_aligned(gate, gate_stride, 0, sx, 16)) &&
+                      (!y || rows_aligned(y, y_stride, 0, sy, ya)) && (!sum_out || rows_aligned(sum_out, sum_stride, 0, sx, 16));
+    return status(wq::launch_block_norm(a, x_dtype, y ? y_dtype : WQ_DT_F32, wide, wq::device_cus(device), (hipStream_t)hip_stream));
+}
+
 int wq_rope_create(int rot, int pairing, double theta, const int *sections, int axes, wq_rope **rope) {
     if (rope == nullptr || sections == nullptr || rot <= 0 || rot % 2 != 0 || (pairing != 0 && pairing != 1) ||
         axes <= 0 || !(theta > 0.0) || !std::isfinite(theta))
@@ -291,6 +313,51 @@ int wq_kv_append_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const v
                      int dtype, long tok, long head, void *hip_stream) {
     return kv_copy(cache, batch, const_cast<void *>(k_new), const_cast<void *>(v_new), dtype, tok, head, true,
                    (hipStream_t)hip_stream);
+}
+
+int wq_kv_append_rope_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const wq_rope *rope, const void *q, int H,
+                          long q_tok, long q_head, void *q_out, long qo_tok, long qo_head, const void *k_new, const void *v_new,
+                          int dtype, long tok, long head, const int *pos_dev, long pos_stride, void *hip_stream) {
+    int rc = check_cache(cache);
+    if (rc == WQ_OK) rc = check_batch(batch);
+    if (rc != WQ_OK) return rc;
+    if (rope == nullptr || rope->magic != kRopeMagic || rope->rot > cache->dim || !float_type(dtype) || tok < 0 || head < 0 ||
+        (q == nullptr) != (q_out == nullptr) || (pos_dev == nullptr && rope->axes != 1) || pos_stride < 0)
+        return WQ_E_INVAL;
+    if (q && (H <= 0 || q_tok < 0 || q_head < 0 || qo_tok < 0 || qo_head < 0)) return WQ_E_INVAL;
+    if (q && H > WQ_KV_MAX_HEADS) return WQ_E_UNSUPPORTED;
+    if (batch->T == 0) return WQ_OK;
+    const int size = size_of(dtype);
+    if (k_new == nullptr || v_new == nullptr || !aligned(k_new, size) || !aligned(v_new, size) || !aligned(q, size) ||
+        !aligned(q_out, size) || !aligned(pos_dev, 4))
+        return WQ_E_INVAL;
+    if ((rc = wq::begin_call(cache->device)) != WQ_OK) return rc;
+    DeviceScope scope(cache->device);
+    wq::KvRopeArgs a;
+    a.c = view(cache);
+    a.b = view(batch);
+    a.q = q;
+    a.k = k_new;
+    a.v = v_new;
+    a.q_out = q_out;
+    a.pos = pos_dev;
+    a.pos_stride = pos_stride;
+    a.qt = q_tok;
+    a.qh = q_head;
+    a.ot = qo_tok;
+    a.oh = qo_head;
+    a.tok = tok;
+    a.head = head;
+    a.H = H;
+    a.rot = rope->rot;
+    a.pairing = rope->pairing;
+    for (int i = 0; i < rope->rot / 2; ++i) {
+        a.turns[i] = rope->turns[i];
+        a.axis[i] = rope->axis[i];
+    }
+    const bool vec = rows_aligned(k_new, tok, head, size, 16) && aligned(v_new, 16) &&
+                     (!q || (rows_aligned(q, q_tok, q_head, size, 16) && rows_aligned(q_out, qo_tok, qo_head, size, 16)));
+    return status(wq::launch_kv_append_rope(a, cache->kind, cache->dim, dtype, vec, wq::device_cus(cache->device), (hipStream_t)hip_stream));
 }
 
 int wq_kv_read_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, void *k_out, void *v_out, int dtype, long tok,

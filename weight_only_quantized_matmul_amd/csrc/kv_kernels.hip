@@ -7,39 +7,12 @@
 // by the chain lengths -> table -> row). Reading 131072 tokens of 8 heads x 128
 // from int8 to bf16: 814 MB in 166 us (4.9 TB/s; one row a lane group 290 us);
 // a decode step of 64 tokens 4 us each way.
-#include "decoder.h"
+#include "kv_rows.h"
 
 namespace wq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kTiny = 0x1p-100f;
-
-template <int KIND>
-struct Codes { // 8 codes
-    static constexpr int bytes = KIND == WQ_KV_F16 ? 16 : KIND == WQ_KV_I8 ? 8 : 4;
-};
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, float *v) {
-    if (VEC) {
-        load_vec<T, 8>(p, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)p[i];
-    }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *p, const float *v) {
-    if (VEC) {
-        store_vec<T, 8>(p, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = (T)v[i];
-    }
-}
-
 // What a lane group works on: a token and its rows first .. first + RPG - 1,
 // keys of all heads before values of all heads.
 struct Where {
@@ -87,14 +60,6 @@ __device__ __forceinline__ void locate(const KvCopyArgs &a, Where &w, int lane) 
     }
 }
 
-// The largest over a group of LANES lanes.
-template <int LANES>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int m = LANES / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
-}
-
 template <typename T, int KIND, int D, bool VEC, int RPG>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvCopyArgs a) {
     constexpr int LANES = D / 8;
@@ -113,52 +78,11 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvCopyArgs a)
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const int s = w.first + j, side = s >= H, head = s - side * H;
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[j][i]));
-        // a NaN is not seen by the maximum: its lane hands on an infinity
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) nan = nan || v[j][i] != v[j][i];
-        top = group_max<LANES>(nan ? INFINITY : top);
+        const float top = row_top<LANES>(v[j]);
         if (!w.there || s >= 2 * H) continue;
         uint8_t *row = const_cast<uint8_t *>(side ? a.c.v : a.c.k) + w.row + head * a.c.rh + (long)lane * Codes<KIND>::bytes;
-        const bool bad = !(top < INFINITY), zero = bad || top < kTiny;
-        float scale;
-        if constexpr (KIND == WQ_KV_F16) {
-            typedef f16 f16x8 __attribute__((ext_vector_type(8)));
-            const int e = ilogbf(top) - 14;
-            scale = ldexpf(1.0f, e);
-            f16x8 c;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = zero ? (f16)0.f : (f16)ldexpf(v[j][i], -e); // exact but for the half's own rounding
-            *reinterpret_cast<f16x8 *>(row) = c;
-        } else {
-            constexpr int N = KIND == WQ_KV_I8 ? 127 : 7;
-            scale = (float)((double)top / N);
-            const float inv = 1.0f / scale;
-            int c[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = v[j][i] * inv; // within N * 3 * 2^-24 of the quotient
-                float q = rintf(f);
-                if (fabsf(f - q) > 0.4999f) q = (float)rint((double)v[j][i] / (double)scale); // next to a border
-                c[i] = zero ? 0 : (int)q;
-            }
-            if constexpr (KIND == WQ_KV_I8) {
-                uint32_t u[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    u[k] = (c[4 * k] & 255) | (c[4 * k + 1] & 255) << 8 | (c[4 * k + 2] & 255) << 16 | (uint32_t)c[4 * k + 3] << 24;
-                *reinterpret_cast<uint2 *>(row) = make_uint2(u[0], u[1]);
-            } else {
-                uint32_t u = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u |= (uint32_t)(c[i] + 8) << (4 * i);
-                *reinterpret_cast<uint32_t *>(row) = u;
-            }
-        }
-        if (lane == 0) const_cast<float *>(side ? a.c.vs : a.c.ks)[w.scale + head * a.c.sh] = bad ? NAN : zero ? 0.f : scale;
+        const float scale = store_codes<KIND>(row, v[j], top);
+        if (lane == 0) const_cast<float *>(side ? a.c.vs : a.c.ks)[w.scale + head * a.c.sh] = scale;
     }
 }
 

@@ -1,0 +1,168 @@
+// C entry points of the mixture-of-experts operators (include/wqmm.h): argument checks and launches.
+#include <climits>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "entry.h"
+#include "moe.h"
+
+namespace {
+
+bool resident(const wq_tensor *t) { return t != nullptr && t->magic == wq::kTensorMagic; }
+
+wq::MoeShape shape_of(const wq_tensor *t) {
+    wq::MoeShape s;
+    s.O = t->O;
+    s.I = t->I;
+    s.stride = (int)t->stride;
+    s.nfull = t->nfull;
+    s.gs = t->gs;
+    s.ng = t->ng;
+    s.steps = (int)((t->stride + 127) / 128);
+    s.kp = s.steps * 128 * wq::elems_per_byte(t->fmt);
+    return s;
+}
+
+bool alike(const wq_tensor *a, const wq_tensor *b) {
+    return a->device == b->device && a->fmt == b->fmt && a->O == b->O && a->I == b->I && a->gs == b->gs;
+}
+
+// A matrix whose bytes 32-bit offsets address and whose positions an int counts.
+bool small(const wq_tensor *t) { return (double)t->O * t->stride < 4294967296.0 && t->stride <= (1 << 28); }
+
+wq::MoeMatrix matrix_of(const wq_tensor *t) {
+    wq::MoeMatrix m;
+    m.w = t->d_w;
+    m.scales = t->gs > 0 ? t->d_scales_t : t->d_scales;
+    return m;
+}
+
+} // namespace
+
+extern "C" {
+
+int wq_moe_route_dev(int device, const void *scores, int dtype, int T, int E, long stride, const float *bias, int gating,
+                     int groups, int top_groups, int k, int normalise, float scale, int *ids, float *weights,
+                     void *hip_stream) {
+    if (!float_type(dtype) || T < 0 || E <= 0 || stride < 0 || k <= 0 || k > E || groups <= 0 || E % groups != 0 ||
+        top_groups <= 0 || top_groups > groups || (gating != WQ_GATE_SOFTMAX && gating != WQ_GATE_SIGMOID) || !std::isfinite(scale))
+        return WQ_E_INVAL;
+    if ((long)(E / groups) * top_groups < k) return WQ_E_INVAL;
+    if (E > WQ_MOE_MAX_EXPERTS || k > WQ_MOE_MAX_K || groups > WQ_MOE_MAX_GROUPS) return WQ_E_UNSUPPORTED;
+    if (T == 0) return WQ_OK;
+    if (scores == nullptr || ids == nullptr || weights == nullptr || !aligned(scores, size_of(dtype)) || !aligned(bias, 4) ||
+        !aligned(ids, 4) || !aligned(weights, 4))
+        return WQ_E_INVAL;
+    const int rc = wq::begin_call(device);
+    if (rc != WQ_OK) return rc;
+    DeviceScope scope(device);
+    wq::RouteArgs a;
+    a.scores = scores;
+    a.stride = stride;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.groups = top_groups == groups ? 1 : groups; // all of them: no choice among groups
+    a.top_groups = top_groups == groups ? 1 : top_groups;
+    a.sigmoid = gating == WQ_GATE_SIGMOID;
+    a.normalise = normalise != 0;
+    a.scale = scale;
+    return status(wq::launch_route(a, dtype, (hipStream_t)hip_stream));
+}
+
+int wq_moe_create(wq_tensor *const *gate, wq_tensor *const *up, wq_tensor *const *down, int E, wq_moe **moe) {
+    if (gate == nullptr || up == nullptr || down == nullptr || moe == nullptr || E <= 0) return WQ_E_INVAL;
+    if (E > WQ_MOE_MAX_EXPERTS) return WQ_E_UNSUPPORTED;
+    for (int e = 0; e < E; ++e) {
+        if (!resident(gate[e]) || !resident(up[e]) || !resident(down[e])) return WQ_E_INVAL;
+        if (!alike(gate[e], gate[0]) || !alike(up[e], gate[0]) || !alike(down[e], down[0])) return WQ_E_INVAL;
+    }
+    if (down[0]->device != gate[0]->device || down[0]->fmt != gate[0]->fmt || down[0]->I != gate[0]->O) return WQ_E_INVAL;
+    if (gate[0]->fmt == WQ_F32 || !small(gate[0]) || !small(down[0])) return WQ_E_UNSUPPORTED;
+    const int device = gate[0]->device;
+    if (!wq::device_is_open(device)) return WQ_E_NOTINIT;
+    DeviceScope scope(device);
+    wq_moe *m = new (std::nothrow) wq_moe;
+    wq::MoeExpert *table = new (std::nothrow) wq::MoeExpert[E];
+    int rc = m == nullptr || table == nullptr ? WQ_E_OOM : WQ_OK;
+    if (rc == WQ_OK) {
+        for (int e = 0; e < E; ++e) {
+            table[e].gate = matrix_of(gate[e]);
+            table[e].up = matrix_of(up[e]);
+            table[e].down = matrix_of(down[e]);
+        }
+        rc = wq::device_table(device, table, (size_t)E * sizeof(wq::MoeExpert), (void **)&m->d_experts);
+    }
+    delete[] table;
+    if (rc != WQ_OK) {
+        delete m;
+        return rc;
+    }
+    m->magic = wq::kMoeMagic;
+    m->device = device;
+    m->fmt = gate[0]->fmt;
+    m->E = E;
+    m->in = shape_of(gate[0]);
+    m->out = shape_of(down[0]);
+    *moe = m;
+    return WQ_OK;
+}
+
+int wq_moe_free(wq_moe *moe) {
+    if (moe == nullptr) return WQ_OK;
+    if (moe->magic != wq::kMoeMagic) return WQ_E_INVAL;
+    DeviceScope scope(moe->device);
+    wq::device_table_free(moe->device, moe->d_experts, (size_t)moe->E * sizeof(wq::MoeExpert));
+    moe->magic = 0;
+    delete moe;
+    return WQ_OK;
+}
+
+int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
+                   int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream) {
+    if (moe == nullptr || moe->magic != wq::kMoeMagic || !float_type(dtype) || T < 0 || k <= 0 || x_stride < 0 ||
+        y_stride < 0 || (add && add_stride < 0))
+        return WQ_E_INVAL;
+    if ((long)T * k > WQ_MOE_MAX_ROWS) return WQ_E_UNSUPPORTED;
+    if (T == 0) return WQ_OK;
+    const int size = size_of(dtype);
+    if (x == nullptr || y == nullptr || ids == nullptr || weights == nullptr || !aligned(x, size) || !aligned(y, size) ||
+        !aligned(add, size) || !aligned(ids, 4) || !aligned(weights, 4))
+        return WQ_E_INVAL;
+    int rc = wq::begin_call(moe->device);
+    if (rc != WQ_OK) return rc;
+    DeviceScope scope(moe->device);
+    wq::MoeArgs a;
+    a.experts = moe->d_experts;
+    a.E = moe->E;
+    a.T = T;
+    a.k = k;
+    a.ids = ids;
+    a.weights = weights;
+    a.x = x;
+    a.add = add;
+    a.y = y;
+    a.xs = x_stride;
+    a.as = add_stride;
+    a.ys = y_stride;
+    a.in = moe->in;
+    a.out = moe->out;
+    a.planes = dtype == WQ_DT_F32 ? 3 : dtype == WQ_DT_F16 ? 2 : 1;
+    const long N = (long)T * k;
+    const size_t plan = (size_t)wq::round_up(4 * wq::plan_ints(a.E, N), 256);
+    const size_t xp = (size_t)wq::round_up(2L * T * a.planes * a.in.kp, 256);
+    const size_t hp = (size_t)wq::round_up(2L * N * 3 * a.out.kp, 256);
+    void *ws = nullptr;
+    if ((rc = wq::stream_workspace(moe->device, plan + xp + hp + 4ul * N * a.out.O, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
+    a.plan = (int *)ws;
+    a.xp = (uint16_t *)((char *)ws + plan);
+    a.hp = (uint16_t *)((char *)ws + plan + xp);
+    a.d = (float *)((char *)ws + plan + xp + hp);
+    return status(wq::launch_moe(a, moe->fmt, dtype, (hipStream_t)hip_stream));
+}
+
+} // extern "C"

@@ -1,0 +1,178 @@
+// The choice of a token's experts from the router's scores.
+//
+// A wave takes one token; expert e is in lane e % 64. Probabilities and the
+// values that decide the choice are fp64, so that the choice is the one the
+// definition makes whatever the scores' type, and the weights are rounded
+// once. Groups are valued by their two largest experts, lanes sharing a group;
+// the k largest are then found one after another, the lowest expert first
+// among equals.
+#include "moe.h"
+
+namespace wq {
+namespace {
+
+constexpr int kWaves = 4; // tokens a block
+
+// Order-preserving code of a double (no NaN): larger values have larger codes, and every code is above 0.
+__device__ __forceinline__ uint64_t order(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0); // -0 counts as 0
+    return u >> 63 ? ~u : u | 1ull << 63;
+}
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) {
+    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), m) << 32 | (uint32_t)__shfl_xor((int)v, m);
+}
+
+// NPL: experts a lane
+template <typename T, int NPL>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(const RouteArgs a) {
+    extern __shared__ double lds[]; // with groups: E values a wave
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long tok = (long)blockIdx.x * kWaves + wave;
+    if (tok >= a.T) return; // (waves share nothing: no barrier below)
+    const T *row = (const T *)a.scores + tok * a.stride;
+    float x[NPL];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = i * 64 + lane;
+        x[i] = e < a.E ? (float)row[e] : -INFINITY;
+        x[i] = x[i] != x[i] ? -INFINITY : fminf(x[i], 3.402823466e+38f);
+        top = fmaxf(top, x[i]);
+    }
+    double p[NPL];
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) p[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+    } else {
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            p[i] = top == -INFINITY ? 0.0 : exp((double)x[i] - (double)top); // no expert has a score: no probability
+            sum += p[i];
+        }
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+        if (sum == 0.0) sum = 1.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) p[i] /= sum;
+    }
+    uint64_t key[NPL]; // 0: not to be chosen
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = i * 64 + lane;
+        double c = p[i] + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
+        if (c != c) c = -INFINITY;
+        key[i] = e < a.E ? order(c) : 0;
+        if (a.groups > 1 && e < a.E) lds[wave * a.E + e] = c;
+    }
+    if (a.groups > 1) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int n = a.E / a.groups;
+        int L = 64; // lanes a group
+        while (L * a.groups > 64) L >>= 1;
+        const int grp = lane / L;
+        double one = -INFINITY, two = -INFINITY; // the group's largest, and the next
+        if (grp < a.groups)
+            for (int i = lane & (L - 1); i < n; i += L) {
+                const double c = lds[wave * a.E + grp * n + i];
+                two = fmax(two, fmin(one, c));
+                one = fmax(one, c);
+            }
+        for (int m = L >> 1; m > 0; m >>= 1) {
+            const double o1 = __shfl_xor(one, m), o2 = __shfl_xor(two, m);
+            two = fmax(fmin(one, o1), fmax(two, o2));
+            one = fmax(one, o1);
+        }
+        double value = n > 1 ? one + two : one;
+        if (value != value) value = -INFINITY;
+        int before = 0; // groups that go before this one
+        for (int g = 0; g < a.groups; ++g) {
+            const double v = __shfl(value, g * L);
+            before += v > value || (v == value && g < grp);
+        }
+        const uint64_t kept = __ballot(grp < a.groups && before < a.top_groups && (lane & (L - 1)) == 0);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = i * 64 + lane;
+            if (e < a.E && !(kept >> (e / n * L) & 1)) key[i] = 0;
+        }
+    }
+    int id = 0;
+    double w = 0.0;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = 0;
+        int e = 1 << 30;
+        double pe = 0.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                e = i * 64 + lane;
+                pe = p[i];
+            }
+        uint64_t most = best;
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) {
+            const uint64_t o = shfl_xor64(most, m);
+            most = o > most ? o : most;
+        }
+        int first = best == most ? e : 1 << 30;
+        const uint64_t ties = __ballot(best == most);
+        if (ties & (ties - 1)) { // several lanes: the lowest expert
+#pragma unroll
+            for (int m = 32; m > 0; m >>= 1) first = min(first, __shfl_xor(first, m));
+        } else {
+            first = __shfl(first, __builtin_ctzll(ties));
+        }
+        pe = __shfl(pe, first & 63);
+        if (lane == j) {
+            id = first;
+            w = pe;
+        }
+        if (lane == (first & 63)) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (i == first >> 6) key[i] = 0;
+        }
+    }
+    if (a.normalise) {
+        double sum = lane < a.k ? w : 0.0;
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+        w = sum > 0.0 ? w / sum : 0.0;
+    }
+    if (lane < a.k) {
+        a.ids[tok * a.k + lane] = id;
+        a.weights[tok * a.k + lane] = (float)(w * (double)a.scale);
+    }
+}
+
+template <typename T>
+hipError_t launch_t(const RouteArgs &a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.T + (long)kWaves - 1) / kWaves)), block(64 * kWaves);
+    const size_t lds = a.groups > 1 ? sizeof(double) * kWaves * a.E : 0;
+#define WQ_ROUTE(N)                                                                                                    \
+    if (a.E <= 64 * N) {                                                                                               \
+        hipLaunchKernelGGL((route_kernel<T, N>), grid, block, lds, st, a);                                             \
+        return hipGetLastError();                                                                                      \
+    }
+    WQ_ROUTE(1) WQ_ROUTE(2) WQ_ROUTE(4) WQ_ROUTE(8) WQ_ROUTE(16)
+#undef WQ_ROUTE
+    return hipErrorInvalidValue;
+}
+
+} // namespace
+
+hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t st) {
+    switch (dtype) {
+    case WQ_DT_F32: return launch_t<float>(a, st);
+    case WQ_DT_BF16: return launch_t<bf16>(a, st);
+    default: return launch_t<f16>(a, st);
+    }
+}
+
+} // namespace wq

@@ -375,6 +375,27 @@ int stream_workspace(int device, size_t bytes, hipStream_t st, void **out) {
 
 int device_cus(int device) { return g_dev[device].cus; }
 
+bool device_is_open(int device) { return device_open(device); }
+
+int device_table(int device, const void *host, size_t bytes, void **out) {
+    DeviceCtx &d = g_dev[device];
+    std::lock_guard<std::recursive_mutex> lk(d.mu);
+    const int rc = dev_alloc(d, out, bytes);
+    if (rc != WQ_OK) return rc;
+    hipError_t e = hipMemcpyAsync(*out, host, bytes, hipMemcpyHostToDevice, d.stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(d.stream);
+    if (e == hipSuccess) return WQ_OK;
+    dev_free(d, *out, bytes);
+    *out = nullptr;
+    return hip_status(e);
+}
+
+void device_table_free(int device, void *p, size_t bytes) {
+    DeviceCtx &d = g_dev[device];
+    std::lock_guard<std::recursive_mutex> lk(d.mu);
+    dev_free(d, p, bytes);
+}
+
 } // namespace wq
 
 extern "C" {
