@@ -58,16 +58,22 @@ def silu(z):
         return z / (1 + np.exp(-z))
 
 
+def product(x, Ex, w):
+    """(x @ w.T, bound) of x float64 [S, I] that is itself within Ex: sums within 1e-5 of the sum of the terms' magnitudes (the
+    matmuls' contract), and activations as integers of 31 bits: within 2^-31 of the largest that shares their unit, here of all."""
+    a, near = np.abs(w).T, np.abs(x) + Ex
+    return x @ w.T, 1e-5 * (near @ a) + Ex @ a + 2.0 ** -31 * near.max(1, keepdims=True) * a.sum(0) + 1e-30
+
+
 def expert_rows(x, gate, up, down):
-    """(y, bound) of one expert's feed-forward of x float64 [S, D]: every product within 1e-5 of the sum of its terms'
-    magnitudes (the matmuls' contract), silu's slope at most 1.1, fp32's silu and product within 2e-6."""
-    g, u = x @ gate.T, x @ up.T
-    Eg, Eu = 1e-5 * (np.abs(x) @ np.abs(gate).T) + 1e-30, 1e-5 * (np.abs(x) @ np.abs(up).T) + 1e-30
+    """(y, bound) of one expert's feed-forward of x float64 [S, D]: products as above, silu's slope at most 1.1, fp32's silu and
+    product within 2e-6."""
+    none = np.zeros_like(x)
+    (g, Eg), (u, Eu) = product(x, none, gate), product(x, none, up)
     h = silu(g) * u
     Eh = 1.1 * Eg * (np.abs(u) + Eu) + np.abs(silu(g)) * Eu
     Eh += 2e-6 * (np.abs(h) + Eh) + 1e-30
-    a = np.abs(down).T
-    return h @ down.T, 1e-5 * ((np.abs(h) + Eh) @ a) + Eh @ a + 1e-30
+    return product(h, Eh, down)
 
 
 def moe(x, ids, weights, mats, add=None):

@@ -58,27 +58,40 @@ struct RouteArgs {
 hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t st);
 
 // ---------------------------------------------------------------------------
+// A chosen expert: its matrices, how many rows it has, and where their slots t * k + j stand in the order of all slots by expert.
+struct MoeWork {
+    MoeExpert e;
+    int rows, first;
+    int pad[2];
+};
+
 struct MoeArgs {
     const MoeExpert *experts;
-    int E, T, k;
+    int E, T, k, cus;
     const int *ids;       // [T, k]
     const float *weights; // [T, k]
     const void *x, *add;
     void *y;
     long xs, as, ys;
     MoeShape in, out;
-    int planes; // bf16 parts of an element of x: 3 (f32), 2 (f16), 1 (bf16)
+    // x as the products read it: rows of xe_n elements (a multiple of four, zeros behind x's own) of x_size bytes, four-aligned
+    const void *xe;
+    long xes;
+    int xe_n, x_size;
+    bool x_bf16;
+    int ldh;                 // floats a row of h, a multiple of four
+    int tiles_in, tiles_out; // tiles of outputs a block of the products takes
     // workspace
-    int *plan;        // plan_ints(E, N)
-    uint16_t *xp;     // [T][planes][in.kp]
-    uint16_t *hp;     // [N][3][out.kp]
-    float *d;         // [N][out.O]
+    MoeWork *plan; // min(E, N), those without rows last; null: the products' blocks plan for themselves
+    int *order;    // N slots, with a plan
+    void *copy;    // x in rows that can be read four at a time; null: they can
+    float *h;      // [N][ldh]
+    float *d;      // [N][out.O]
 };
 
-// The plan: number of chosen experts, then three ints each (expert, first place in the order, rows), then the slots
-// t * k + j sorted by expert.
-__host__ __device__ inline long plan_ints(int E, long N) { return 4 + 3L * E + N; }
-
-hipError_t launch_moe(const MoeArgs &a, int fmt, int dtype, hipStream_t st);
+hipError_t launch_moe(MoeArgs &a, int fmt, int dtype, hipStream_t st);
+hipError_t launch_moe_i8(MoeArgs &a, hipStream_t st);
+hipError_t launch_moe_i4(MoeArgs &a, hipStream_t st);
+hipError_t launch_moe_i2(MoeArgs &a, hipStream_t st);
 
 } // namespace wq

@@ -139,6 +139,7 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     wq::MoeArgs a;
     a.experts = moe->d_experts;
     a.E = moe->E;
+    a.cus = wq::device_cus(moe->device);
     a.T = T;
     a.k = k;
     a.ids = ids;
@@ -151,17 +152,28 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     a.ys = y_stride;
     a.in = moe->in;
     a.out = moe->out;
-    a.planes = dtype == WQ_DT_F32 ? 3 : dtype == WQ_DT_F16 ? 2 : 1;
     const long N = (long)T * k;
-    const size_t plan = (size_t)wq::round_up(4 * wq::plan_ints(a.E, N), 256);
-    const size_t xp = (size_t)wq::round_up(2L * T * a.planes * a.in.kp, 256);
-    const size_t hp = (size_t)wq::round_up(2L * N * 3 * a.out.kp, 256);
+    a.x_size = size;
+    a.x_bf16 = dtype == WQ_DT_BF16;
+    a.xe_n = (a.in.I + 3) / 4 * 4;
+    a.ldh = (a.in.O + 3) / 4 * 4;
+    const bool apart = a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size);
+    // up to 64 slots every block of the products finds its expert's rows for itself
+    const bool planned = N > 64 || apart;
+    const size_t plan = planned ? (size_t)wq::round_up((N < a.E ? N : a.E) * sizeof(wq::MoeWork), 256) : 0;
+    const size_t order = planned ? (size_t)wq::round_up(4 * N, 256) : 0;
+    const size_t copy = apart ? (size_t)wq::round_up((long)T * a.xe_n * size, 256) : 0;
+    const size_t h = (size_t)wq::round_up(4 * N * a.ldh, 256);
     void *ws = nullptr;
-    if ((rc = wq::stream_workspace(moe->device, plan + xp + hp + 4ul * N * a.out.O, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
-    a.plan = (int *)ws;
-    a.xp = (uint16_t *)((char *)ws + plan);
-    a.hp = (uint16_t *)((char *)ws + plan + xp);
-    a.d = (float *)((char *)ws + plan + xp + hp);
+    if ((rc = wq::stream_workspace(moe->device, plan + order + copy + h + 4ul * N * a.out.O, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
+    char *at = (char *)ws;
+    a.plan = planned ? (wq::MoeWork *)at : nullptr;
+    a.order = (int *)(at += plan);
+    a.copy = apart ? at + order : nullptr;
+    a.h = (float *)(at += order + copy);
+    a.d = (float *)(at += h);
+    a.xe = apart ? a.copy : x;
+    a.xes = apart ? a.xe_n : x_stride;
     return status(wq::launch_moe(a, moe->fmt, dtype, (hipStream_t)hip_stream));
 }
 
