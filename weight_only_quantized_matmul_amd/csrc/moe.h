@@ -80,6 +80,8 @@ struct MoeArgs {
     int xe_n, x_size;
     bool x_bf16;
     int ldh;                 // floats a row of h, a multiple of four
+    int active;              // experts that some token chose, on average of an even choice
+    int operands;            // of 16 stacked rows, four activations each, that the products take at a time: 1, 2; 4, 8: prepared parts
     int tiles_in, tiles_out; // tiles of outputs a block of the products takes
     // workspace
     MoeWork *plan; // min(E, N), those without rows last; null: the products' blocks plan for themselves
@@ -87,6 +89,8 @@ struct MoeArgs {
     void *copy;    // x in rows that can be read four at a time; null: they can
     float *h;      // [N][ldh]
     float *d;      // [N][out.O]
+    uint8_t *xp, *hp;      // parts: [T][in.steps] and [N][out.steps] times four planes of a step's positions
+    float *xunit, *hunit;  // [T][in.steps], [N][out.steps]
 };
 
 hipError_t launch_moe(MoeArgs &a, int fmt, int dtype, hipStream_t st);

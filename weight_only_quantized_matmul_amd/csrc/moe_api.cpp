@@ -157,21 +157,35 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     a.x_bf16 = dtype == WQ_DT_BF16;
     a.xe_n = (a.in.I + 3) / 4 * 4;
     a.ldh = (a.in.O + 3) / 4 * 4;
-    const bool apart = a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size);
+    a.active = (int)(a.E * (1.0 - std::pow(1.0 - (k < a.E ? k : a.E) / (double)a.E, T)) + 0.5);
+    if (a.active < 1) a.active = 1;
+    // operands for the rows that an expert has on average, with room for those that have more
+    const double rows = (double)N / a.active;
+    a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
+    const bool parts = a.operands >= 4;
+    const bool apart = !parts && (a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size));
     // up to 64 slots every block of the products finds its expert's rows for itself
-    const bool planned = N > 64 || apart;
+    const bool planned = N > 64 || apart || parts;
     const size_t plan = planned ? (size_t)wq::round_up((N < a.E ? N : a.E) * sizeof(wq::MoeWork), 256) : 0;
     const size_t order = planned ? (size_t)wq::round_up(4 * N, 256) : 0;
     const size_t copy = apart ? (size_t)wq::round_up((long)T * a.xe_n * size, 256) : 0;
     const size_t h = (size_t)wq::round_up(4 * N * a.ldh, 256);
+    const int epb = wq::elems_per_byte(moe->fmt);
+    const size_t d = (size_t)wq::round_up(4 * N * a.out.O, 256);
+    const size_t xp = parts ? (size_t)T * a.in.steps * 512 * epb : 0, hp = parts ? (size_t)N * a.out.steps * 512 * epb : 0;
+    const size_t xu = parts ? (size_t)wq::round_up(4L * T * a.in.steps, 256) : 0, hu = parts ? (size_t)4 * N * a.out.steps : 0;
     void *ws = nullptr;
-    if ((rc = wq::stream_workspace(moe->device, plan + order + copy + h + 4ul * N * a.out.O, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
+    if ((rc = wq::stream_workspace(moe->device, plan + order + copy + h + d + xp + hp + xu + hu, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
     char *at = (char *)ws;
     a.plan = planned ? (wq::MoeWork *)at : nullptr;
     a.order = (int *)(at += plan);
     a.copy = apart ? at + order : nullptr;
     a.h = (float *)(at += order + copy);
     a.d = (float *)(at += h);
+    a.xp = parts ? (uint8_t *)at + d : nullptr;
+    a.hp = a.xp + xp;
+    a.xunit = (float *)(at + d + xp + hp);
+    a.hunit = (float *)(at + d + xp + hp + xu);
     a.xe = apart ? a.copy : x;
     a.xes = apart ? a.xe_n : x_stride;
     return status(wq::launch_moe(a, moe->fmt, dtype, (hipStream_t)hip_stream));

@@ -8,15 +8,15 @@
 // the products of down write one row a slot; and the last kernel adds each
 // token's rows in the order of its slots, so results do not depend on what
 // else the batch holds.
-#include "moe.h"
+#include "moe_parts.h"
 
 namespace wq {
 namespace {
 
 constexpr int kPrepThreads = 512;
 
-// Block 0 makes the plan; the others copy x where its rows cannot be read four elements at a time.
-template <typename T>
+// Block 0 makes the plan; the others make x's parts, or copy x where its rows cannot be read four elements at a time.
+template <int FMT, typename T>
 __global__ __launch_bounds__(kPrepThreads) void moe_prepare_kernel(const MoeArgs a) {
     __shared__ int cnt[WQ_MOE_MAX_EXPERTS], at[WQ_MOE_MAX_EXPERTS];
     __shared__ uint32_t part[kPrepThreads / 64];
@@ -66,6 +66,14 @@ __global__ __launch_bounds__(kPrepThreads) void moe_prepare_kernel(const MoeArgs
         }
         return;
     }
+    if (a.xp != nullptr) {
+        const int per_row = a.in.kp / kPiece;
+        for (long i = (long)(blockIdx.x - 1) * kPrepThreads + tid; i < (long)a.T * per_row; i += (long)(gridDim.x - 1) * kPrepThreads) {
+            const long row = i / per_row;
+            prepare_piece<FMT>((const T *)a.x + row * a.xs, a.in.I, a.in, row, (int)(i - row * per_row) * kPiece, a.xp, a.xunit);
+        }
+        return;
+    }
     const long items = (long)a.T * a.xe_n;
     for (long i = (long)(blockIdx.x - 1) * kPrepThreads + tid; i < items; i += (long)(gridDim.x - 1) * kPrepThreads) {
         const int t = (int)(i / a.xe_n), e = (int)(i - (long)t * a.xe_n);
@@ -100,9 +108,15 @@ template <typename T>
 hipError_t launch_t(MoeArgs &a, int fmt, hipStream_t st) {
     hipError_t e = hipSuccess;
     if (a.plan != nullptr) {
-        const long blocks = a.copy ? ((long)a.T * a.xe_n + kPrepThreads - 1) / kPrepThreads : 0;
+        const long items = a.xp ? (long)a.T * (a.in.kp / kPiece) : a.copy ? (long)a.T * a.xe_n : 0;
+        const long blocks = (items + kPrepThreads - 1) / kPrepThreads;
         const dim3 grid((unsigned)(1 + (blocks < 1024 ? blocks : 1024)));
-        hipLaunchKernelGGL((moe_prepare_kernel<T>), grid, dim3(kPrepThreads), 0, st, a);
+        if (fmt == WQ_I8)
+            hipLaunchKernelGGL((moe_prepare_kernel<WQ_I8, T>), grid, dim3(kPrepThreads), 0, st, a);
+        else if (fmt == WQ_I4)
+            hipLaunchKernelGGL((moe_prepare_kernel<WQ_I4, T>), grid, dim3(kPrepThreads), 0, st, a);
+        else
+            hipLaunchKernelGGL((moe_prepare_kernel<WQ_I2, T>), grid, dim3(kPrepThreads), 0, st, a);
         e = hipGetLastError();
     }
     if (e == hipSuccess) e = fmt == WQ_I8 ? launch_moe_i8(a, st) : fmt == WQ_I4 ? launch_moe_i4(a, st) : launch_moe_i2(a, st);

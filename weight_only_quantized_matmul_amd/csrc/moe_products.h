@@ -7,27 +7,12 @@
 // 2^-31 of the step's largest magnitude. The integer sums are exact; each step's goes to the fp32 sum with its unit.
 #pragma once
 
-#include <cmath>
 #include <type_traits>
 
-#include "moe.h"
+#include "moe_parts.h"
 
 namespace wq {
 namespace {
-
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-template <int FMT>
-struct Fmt {
-    static constexpr int EPB = FMT == WQ_I8 ? 1 : FMT == WQ_I4 ? 2 : 4;
-    static constexpr int POS = 128 * EPB; // positions of a step
-    static constexpr float UNSCALE = FMT == WQ_I8 ? 1.0f : FMT == WQ_I4 ? 0.0625f : 0.015625f;
-};
-
-// Bytes of b where sel's are 0..3, of a where 4..7.
-__device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t sel) { return __builtin_amdgcn_perm(a, b, sel); }
 
 // How a block's four waves share its work: WR groups of output rows, WK waves along the rows' bytes. A wave has NT tiles of
 // 16 rows of weights (gate and up of the same 16 outputs, or 32 outputs of down), so a block makes 16 * WR (32 * WR) outputs
@@ -48,13 +33,15 @@ struct Products {
     static constexpr int UNITS = F::EPB;                    // products of 64 positions in 64 bytes
     static constexpr bool TURN = GS == 2 && F::EPB > 1;
     static constexpr int RED = kWaves * NT * 64 * 4;        // bytes of the waves' sums
-    static constexpr bool BIG = M == 4;                     // many rows: two blocks a CU with more registers, else three
+    // Many rows: two blocks a CU with more registers, else three; and activations whose parts stand prepared in memory, where
+    // every block would make them again (8 experts of 2048 x 6144 in int8 with 16 rows each: 190 us).
+    static constexpr bool BIG = M >= 3;
     static constexpr int LDS = (BIG ? 74 : 44) * 1024;      // bytes of a phase's parts and units
     static constexpr int UNIT = 4 * (2 * WK * F::POS + 16) + 4 * 2 * WK; // bytes of an activation row with two steps of every wave
     static constexpr int ROWS = LDS / UNIT < 4 * M ? LDS / UNIT : 4 * M; // rows at a time
     static_assert(ROWS >= 1, "a phase holds two steps of every wave");
-    static constexpr int PIECE = 16;                        // positions that a thread stages at a time
-    static constexpr int PRE = 2;                     // pieces of a thread that are loaded ahead of the weights
+    static constexpr int PIECE = kPiece;                    // positions that a thread stages at a time
+    static constexpr int PRE = M == 8 ? 0 : 2;                     // pieces of a thread that are loaded ahead of the weights
 
     const MoeArgs &a;
     const MoeShape &sh;
@@ -72,8 +59,15 @@ struct Products {
         u32x4 v[4];
     };
 
-    // The activations of positions pos .. pos + 15 of a slot.
+    // The activations of positions pos .. pos + 15 of a slot; BIG: their parts.
     __device__ __forceinline__ void fetch(int slot, int pos, Piece &p) const {
+        if constexpr (BIG) {
+            const int step = pos / F::POS;
+            const uint8_t *from = (GATED ? a.xp : a.hp) + ((long)(GATED ? slot / a.k : slot) * sh.steps + step) * (4 * F::POS) + pos % F::POS;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) p.v[q] = step < sh.steps ? *reinterpret_cast<const u32x4 *>(from + q * F::POS) : u32x4{0, 0, 0, 0};
+            return;
+        }
         const bool wide = !GATED || a.x_size == 4;
         const uint8_t *row = GATED ? (const uint8_t *)a.xe + (long)(slot / a.k) * a.xes * a.x_size : (const uint8_t *)(a.h + (long)slot * a.ldh);
         const int end = GATED ? a.xe_n : a.ldh; // elements of a row, a multiple of four
@@ -90,48 +84,27 @@ struct Products {
         }
     }
 
-    // Puts the parts of a piece to `to` (the parts' rows `pitch` bytes apart) and the step's unit to `unit`. The lanes of a
-    // step's pieces come here together.
-    __device__ __forceinline__ void put(const Piece &p, uint8_t *to, int pitch, float *unit) const {
-        float x[16];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint16_t half = (uint16_t)(p.v[q][j >> 1] >> (16 * (j & 1)));
-                x[4 * q + j] = !GATED || a.x_size == 4 ? __uint_as_float(p.v[q][j])
-                               : a.x_bf16              ? __uint_as_float((uint32_t)half << 16)
-                                                       : (float)__builtin_bit_cast(f16, half);
-            }
-        // the step's largest magnitude; NaN and infinities order above all numbers as bits
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int m = F::POS / PIECE / 2; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-        // 2^(e + 1) is above it, and the unit 2^(e - 29) a normal number
-        const int e = max((int)(top >> 23) - 127, -96);
-        const bool bad = top >= 0x7F800000u;
-        const float up = __uint_as_float((uint32_t)(127 + 29 - min(e, 127)) << 23); // 2^(29 - e)
-        *unit = bad ? NAN : __uint_as_float((uint32_t)(127 - 29 + min(e, 127)) << 23) * F::UNSCALE;
-        uint32_t d[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            // balanced digits: the carries of adding 128 to each byte, and 128 off again
-            const int v = bad ? 0 : (int)rintf(x[i] * up);
-            d[i] = ((uint32_t)v + 0x80808080u) ^ 0x80808080u;
-        }
+    // Puts the parts of a piece to `to` (the parts' rows `pitch` bytes apart) and the step's unit to `unit`.
+    __device__ __forceinline__ void put(const Piece &p, int slot, int pos, uint8_t *to, int pitch, float *unit) const {
         u32x4 part[4];
+        if constexpr (BIG) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) { // byte k of the operands' words: in the order in which the codes come out
-            const int s = FMT == WQ_I8 ? 4 * k : FMT == WQ_I4 ? 8 * (k >> 1) + (k & 1) : k, t = FMT == WQ_I8 ? 1 : FMT == WQ_I4 ? 2 : 4;
-            const uint32_t e0 = d[s], e1 = d[s + t], e2 = d[s + 2 * t], e3 = d[s + 3 * t];
-            const uint32_t l01 = bytes(e1, e0, 0x05010400u), h01 = bytes(e1, e0, 0x07030602u);
-            const uint32_t l23 = bytes(e3, e2, 0x05010400u), h23 = bytes(e3, e2, 0x07030602u);
-            part[0][k] = bytes(l23, l01, 0x05040100u);
-            part[1][k] = bytes(l23, l01, 0x07060302u);
-            part[2][k] = bytes(h23, h01, 0x05040100u);
-            part[3][k] = bytes(h23, h01, 0x07060302u);
+            for (int q = 0; q < 4; ++q) part[q] = p.v[q];
+            const int step = pos / F::POS;
+            if (pos % F::POS == 0)
+                *unit = step < sh.steps ? (GATED ? a.xunit : a.hunit)[(long)(GATED ? slot / a.k : slot) * sh.steps + step] : 0.f;
+        } else {
+            float x[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint16_t half = (uint16_t)(p.v[q][j >> 1] >> (16 * (j & 1)));
+                    x[4 * q + j] = !GATED || a.x_size == 4 ? __uint_as_float(p.v[q][j])
+                                   : a.x_bf16              ? __uint_as_float((uint32_t)half << 16)
+                                                           : (float)__builtin_bit_cast(f16, half);
+                }
+            *unit = make_parts<FMT>(x, part);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4 *>(to + q * pitch) = part[q];
@@ -144,7 +117,7 @@ struct Products {
         // a phase: as many steps of all waves as the buffer holds activations of
         const int fit = (LDS / n - 64) / (WK * (4 * F::POS + 4)) & ~1;
         // (BIG: no more than what the threads hold ahead)
-        const int held = BIG ? max(PRE * 64 * kWaves * PIECE / (n * WK * F::POS) & ~1, 2) : fit;
+        const int held = BIG && PRE > 0 ? max(PRE * 64 * kWaves * PIECE / (n * WK * F::POS) & ~1, 2) : fit;
         const int per = min(all, min(fit, held)), phases = (all + per - 1) / per; // per is even
         const int span = per * WK * F::POS, pitch = span + 16;         // positions; bytes of a part's row, 16 apart in the banks
         float *units = reinterpret_cast<float *>(lds + n * 4 * pitch); // [n][per * WK]
@@ -163,7 +136,7 @@ struct Products {
             const int row = last ? rest : whole;
             if (i >= n * row) return;
             const int s = (int)__umulhi((uint32_t)i, last ? by_rest : by_whole), c = PIECE * (i - s * row);
-            put(p, lds + s * 4 * pitch + c, pitch, units + s * per * WK + c / F::POS);
+            put(p, slots[s], ph * span + c, lds + s * 4 * pitch + c, pitch, units + s * per * WK + c / F::POS);
         };
         auto stage = [&](int ph, int from) __attribute__((always_inline)) {
             const int row = ph == phases - 1 ? rest : whole;
@@ -196,7 +169,7 @@ struct Products {
                     to[b][u] = __builtin_nontemporal_load((const GLOBAL u32x4 *)((const GLOBAL uint8_t *)matrix(b).w + (woff[b][u] + byte)));
         };
         // the first phase's activations are asked for ahead of the weights: behind them they would wait for all of those
-        Piece ahead[PRE];
+        Piece ahead[PRE > 0 ? PRE : 1];
 #pragma unroll
         for (int q = 0; q < PRE; ++q) piece(threadIdx.x + q * 64 * kWaves, 0, ahead[q]);
         __builtin_amdgcn_sched_barrier(0);
@@ -230,29 +203,25 @@ struct Products {
                     h[0][b][j] = __builtin_amdgcn_update_dpp(v0, v1, 0x128, 0xF, 0xC, false);
                     h[1][b][j] = __builtin_amdgcn_update_dpp(v1, v0, 0x128, 0xF, 0x3, false);
                 }
-            if constexpr (TURN) { // word j of a half to the four 16-byte pieces number j of its rows
+            if (i + 2 == all) aim(tile + 1); // the next tile's first steps follow
+            load_w(w[SLOT], i + 2 < all ? i + 2 : i + 2 - all);
+            i32x4 part[NT][M];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+            for (int half = 0; half < 2; ++half) {
+                if constexpr (TURN) { // word j of a half to the four 16-byte pieces number j of its rows
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        u32x4 &t = h[u][b];
+                        u32x4 &t = h[half][b];
                         const auto p = __builtin_amdgcn_permlane32_swap(t[0], t[2], false, false), q = __builtin_amdgcn_permlane32_swap(t[1], t[3], false, false);
                         const auto r = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false), s = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
                         t = u32x4{r[0], r[1], s[0], s[1]};
                     }
-            }
-            if (i + 2 == all) aim(tile + 1); // the next tile's first steps follow
-            load_w(w[SLOT], i + 2 < all ? i + 2 : i + 2 - all);
-            float unit[M];
-#pragma unroll
-            for (int m = 0; m < M; ++m) unit[m] = units[xunit[m] + at];
-            i32x4 part[NT][M];
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
+                }
 #pragma unroll
                 for (int u = 0; u < UNITS; ++u) {
                     const uint32_t off = (uint32_t)at * F::POS + half * (F::POS / 2) + (TURN ? 64 : 16) * u;
                     const bool fresh = GS == 0 ? half + u == 0 : TURN || u == 0, last = GS == 0 ? half == 1 && u == UNITS - 1 : TURN || u == UNITS - 1;
+                    if (BIG) __builtin_amdgcn_sched_barrier(0); // (the scheduler would read a whole step's operands at once, and spill)
                     i32x4 x[M];
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
@@ -282,7 +251,9 @@ struct Products {
                             part[b][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[m], q, fresh ? i32x4{0, 0, 0, 0} : part[b][m], 0, 0, 0);
                     }
                     if (last) {
-                        float sc[NT];
+                        float sc[NT], unit[M];
+#pragma unroll
+                        for (int m = 0; m < M; ++m) unit[m] = units[xunit[m] + at];
                         if (GS != 0) {
                             const int pos = (wk + WK * i) * F::POS + half * (F::POS / 2) + (TURN ? 64 * u : 0), grp = min(pos / sh.gs, sh.ng - 1);
 #pragma unroll
@@ -298,8 +269,10 @@ struct Products {
                                 const float v = fmaf(fmaf(fmaf((float)d[3], 256.f, (float)d[2]), 256.f, (float)d[1]), 256.f, (float)d[0]);
                                 acc[b][m] = fmaf(v, GS ? unit[m] * sc[b] : unit[m], acc[b][m]);
                             }
+                        if (BIG) __builtin_amdgcn_sched_barrier(0);
                     }
                 }
+            }
         };
         for (; tile < t1; ++tile) {
 #pragma unroll
@@ -373,7 +346,7 @@ struct Products {
 };
 
 template <int FMT, bool GATED, int GS, int M, int WK, bool INLINE>
-__global__ __launch_bounds__(64 * kWaves, M == 4 ? 2 : 3) void moe_products_kernel(const MoeArgs a) {
+__global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kernel(const MoeArgs a) {
     using P = Products<FMT, GATED, GS, M, WK>;
     __shared__ __align__(16) uint8_t lds[P::LDS];
     __shared__ __align__(16) float red[P::RED / 4];
@@ -425,9 +398,13 @@ hipError_t launch_products(MoeArgs &a, int active, hipStream_t st) {
     per = per < 1 ? 1 : per > tiles ? tiles : per;
     (GATED ? a.tiles_in : a.tiles_out) = per;
     const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)(a.plan == nullptr ? N : N < a.E ? N : a.E));
-    if (a.plan == nullptr)
-        hipLaunchKernelGGL((moe_products_kernel<FMT, GATED, GS, M, WK, true>), grid, dim3(64 * kWaves), 0, st, a);
-    else
+    if constexpr (!P::BIG) {
+        if (a.plan == nullptr) {
+            hipLaunchKernelGGL((moe_products_kernel<FMT, GATED, GS, M, WK, true>), grid, dim3(64 * kWaves), 0, st, a);
+            return hipGetLastError();
+        }
+    }
+    if (a.plan != nullptr)
         hipLaunchKernelGGL((moe_products_kernel<FMT, GATED, GS, M, WK, false>), grid, dim3(64 * kWaves), 0, st, a);
     return hipGetLastError();
 }
@@ -447,12 +424,13 @@ hipError_t launch_wk(MoeArgs &a, int active, hipStream_t st) {
 
 template <int FMT, bool GATED, int GS>
 hipError_t launch_m(MoeArgs &a, hipStream_t st) {
-    // experts that some token chose, on average of an even choice
-    const int active = (int)(a.E * (1.0 - pow(1.0 - (a.k < a.E ? a.k : a.E) / (double)a.E, a.T)) + 0.5);
-    const double rows = (double)a.T * a.k / (active < 1 ? 1 : active);
-    if (a.T <= 4 || rows <= 1.6) return launch_wk<FMT, GATED, GS, 1>(a, active, st);
-    if (a.T <= 8 || rows <= 4) return launch_wk<FMT, GATED, GS, 2>(a, active, st);
-    return launch_wk<FMT, GATED, GS, 4>(a, active, st);
+    switch (a.operands) {
+    case 1: return launch_wk<FMT, GATED, GS, 1>(a, a.active, st);
+    case 2: return launch_wk<FMT, GATED, GS, 2>(a, a.active, st);
+    case 4: return launch_wk<FMT, GATED, GS, GS == 2 ? 3 : 4>(a, a.active, st);
+    default: // (of turned operands, more than three would spill)
+        return launch_wk<FMT, GATED, GS, GS == 2 ? 3 : 8>(a, a.active, st);
+    }
 }
 
 template <int FMT, bool GATED>
@@ -464,9 +442,24 @@ hipError_t launch_gs(MoeArgs &a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
+// h in parts, for many rows. Rows of empty slots hold anything, and their parts are not read.
+template <int FMT>
+__global__ __launch_bounds__(256) void moe_parts_kernel(const MoeArgs a) {
+    const int per_row = a.out.kp / kPiece;
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    const long row = i / per_row;
+    if (row >= (long)a.T * a.k) return;
+    prepare_piece<FMT>(a.h + row * a.ldh, a.in.O, a.out, row, (int)(i - row * per_row) * kPiece, a.hp, a.hunit);
+}
+
 template <int FMT>
 hipError_t launch_both(MoeArgs &a, hipStream_t st) {
-    const hipError_t e = launch_gs<FMT, true>(a, st);
+    hipError_t e = launch_gs<FMT, true>(a, st);
+    if (e == hipSuccess && a.operands >= 4) {
+        const long pieces = (long)a.T * a.k * (a.out.kp / kPiece);
+        hipLaunchKernelGGL((moe_parts_kernel<FMT>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, st, a);
+        e = hipGetLastError();
+    }
     return e == hipSuccess ? launch_gs<FMT, false>(a, st) : e;
 }
 
