@@ -486,7 +486,8 @@ int wq_kv_append_dev(const wq_kv_cache *cache, const wq_kv_batch *batch, const v
  * are turned into q_out (NULL, both: none; q_out may be q with q's strides), the
  * keys k_new are turned, rounded to fp32 and quantised into their slots as by
  * wq_kv_append_dev, the values v_new as they are. Turning follows wq_rope_dev
- * with the plan `rope` (rot <= dim), in fp64 up to that rounding. pos: device
+ * with the plan `rope` (rot <= dim), in fp64 up to that rounding (queries of
+ * 16 bits in fp32). pos: device
  * int32 [axes, T], row stride pos_stride; NULL (plans of one axis only): each
  * token's position p in its sequence. Tokens that have no place in the cache
  * are turned all the same; rows past q_start[B] are left as they were.

@@ -100,7 +100,9 @@ def check_append(c, rng, dtype, rot, pairing, sections, pos=None, H=None, inplac
     if H:
         want = dref.rope(was, p, rot, pairing, THETA, sections)
         # once to fp32, once to the type; the angle's fp64 error grows with the position, which stays below 2^20: 2^-53 * 2^20 * |x|
-        bound = np.abs(want) * (ref.HALF[dtype] + 2.0 ** -23) + 2.0 ** -30 * np.abs(was).max() + ref.TINY[dtype]
+        # queries of 16 bits turn in fp32: the cosine and the sine, two products and their sum are each within 2^-24 of |x|
+        turn = 2.0 ** -30 if dtype == "f32" else 6 * 2.0 ** -24
+        bound = np.abs(want) * (ref.HALF[dtype] + 2.0 ** -23) + turn * np.abs(was).max() + ref.TINY[dtype]
         assert (np.abs(out.double().cpu().numpy() - want) <= bound).all()
         if inplace:
             edge = room.clone()

@@ -5,6 +5,8 @@
 // sine in LDS, of which each thread keeps the ones of its 8 elements for all
 // the rows it takes. Rotated keys are rounded to fp32 and quantised from
 // registers, so they never pass through memory.
+#include <type_traits>
+
 #include "kv_rows.h"
 
 namespace wq {
@@ -19,6 +21,30 @@ __global__ __launch_bounds__(kThreads) void kv_append_rope_kernel(const KvRopeAr
     __shared__ long found; // sequence << 32 | position, or -1
     const int tid = threadIdx.x, lane = tid & (LANES - 1), half = a.rot / 2;
     const int tok = blockIdx.x;
+    const int Hq = a.q ? a.H : 0, rows = Hq + 2 * a.c.heads;
+    const int r0 = (int)((long)rows * blockIdx.y / gridDim.y), r1 = (int)((long)rows * (blockIdx.y + 1) / gridDim.y);
+    // a row's 8 elements and those that they turn with (asked for a round ahead, 2436 tokens took 43 us, with the read, instead of 36)
+    const int e0 = 8 * lane;
+    auto load = [&](int r, float (&v)[8], float (&o)[8]) __attribute__((always_inline)) {
+        const bool is_q = r < Hq, is_v = r >= Hq + a.c.heads;
+        const int head = is_q ? r : is_v ? r - Hq - a.c.heads : r - Hq;
+        const T *x = is_q ? (const T *)a.q + (long)tok * a.qt + (long)head * a.qh
+                          : (const T *)(is_v ? a.v : a.k) + (long)tok * a.tok + (long)head * a.head;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = o[i] = 0.f;
+        if (r >= r1) return;
+        load8<T, VEC>(x + e0, v);
+        if (is_v || e0 >= a.rot || a.pairing == 1) return;
+        if (VEC && half % 8 == 0) {
+            load8<T, VEC>(x + (e0 < half ? e0 + half : e0 - half), o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                o[i] = e < half ? (float)x[e + half] : e < a.rot ? (float)x[e - half] : 0.f;
+            }
+        }
+    };
     if (tid == 0) found = -1;
     __syncthreads();
     for (int i = tid; i < a.b.B; i += kThreads) {
@@ -40,59 +66,56 @@ __global__ __launch_bounds__(kThreads) void kv_append_rope_kernel(const KvRopeAr
     const bool there = find_row(a.c, a.b, seq, t, &page, &slot);
     const long row_at = page * a.c.rp + slot * a.c.rs, scale_at = page * a.c.sp + slot * a.c.ss;
     __syncthreads();
-    // what this thread's elements turn by: y[i] = x[i] * cs[i].x + (the pair's other element) * cs[i].y
-    const int e0 = 8 * lane;
-    double2 cs[8];
+    // What this thread's elements turn by: y[i] = x[i] * cs[i].x + (the pair's other element) * cs[i].y. Queries of 16 bits turn in
+    // fp32, whose error is far below their own rounding; keys, whose codes may lie next to a border, and fp32 queries in fp64.
+    constexpr bool HALF = sizeof(T) == 2;
+    typedef typename std::conditional<HALF, float, double>::type Q;
+    auto turn = [&](int i, double &c, double &s) __attribute__((always_inline)) {
+        const int e = e0 + i, f = a.pairing == 0 ? (e < half ? e : e - half) : e / 2;
+        const bool first = a.pairing == 0 ? e < half : (e & 1) == 0;
+        const double2 w = e < a.rot ? trig[f] : make_double2(1.0, 0.0);
+        c = w.x;
+        s = first ? -w.y : w.y;
+    };
+    Q cs[8][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int e = e0 + i;
-        cs[i] = make_double2(1.0, 0.0);
-        if (e < a.rot) {
-            const int f = a.pairing == 0 ? (e < half ? e : e - half) : e / 2;
-            const bool first = a.pairing == 0 ? e < half : (e & 1) == 0;
-            const double2 w = trig[f];
-            cs[i] = make_double2(w.x, first ? -w.y : w.y);
-        }
+        double c, s;
+        turn(i, c, s);
+        cs[i][0] = (Q)c;
+        cs[i][1] = (Q)s;
     }
-    const int Hq = a.q ? a.H : 0, rows = Hq + 2 * a.c.heads;
-    const int r0 = (int)((long)rows * blockIdx.y / gridDim.y), r1 = (int)((long)rows * (blockIdx.y + 1) / gridDim.y);
-    for (int base = r0; base < r1; base += kThreads / LANES) { // (all lanes of a wave go round together)
+    constexpr int STEP = kThreads / LANES;
+    for (int base = r0; base < r1; base += STEP) { // (all lanes of a wave go round together)
         const int r = base + tid / LANES;
-        const bool live = r < r1;
-        const bool is_q = r < Hq, is_v = r >= Hq + a.c.heads;
+        const bool live = r < r1, is_q = r < Hq, is_v = r >= Hq + a.c.heads;
         const int head = is_q ? r : is_v ? r - Hq - a.c.heads : r - Hq;
-        const T *x = is_q ? (const T *)a.q + (long)tok * a.qt + (long)head * a.qh
-                          : (const T *)(is_v ? a.v : a.k) + (long)tok * a.tok + (long)head * a.head;
-        float v[8];
+        float v[8], o[8], y[8];
+        load(r, v, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        if (live) {
-            load8<T, VEC>(x + e0, v);
-            if (!is_v && e0 < a.rot) {
-                float o[8];
-                if (a.pairing == 1) {
+        for (int i = 0; i < 8; ++i) y[i] = v[i];
+        if (HALF && !is_q && !is_v) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = v[i ^ 1];
-                } else if (VEC && half % 8 == 0) {
-                    load8<T, VEC>(x + (e0 < half ? e0 + half : e0 - half), o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = e0 + i;
-                        o[i] = e < half ? (float)x[e + half] : e < a.rot ? (float)x[e - half] : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (e0 + i < a.rot) v[i] = (float)((double)v[i] * cs[i].x + (double)o[i] * cs[i].y);
+            for (int i = 0; i < 8; ++i) {
+                double c, s;
+                turn(i, c, s);
+                if (e0 + i < a.rot) y[i] = (float)((double)v[i] * c + (double)(a.pairing == 1 ? v[i ^ 1] : o[i]) * s);
             }
-            if (is_q) store8<T, VEC>((T *)a.q_out + (long)tok * a.ot + (long)head * a.oh + e0, v);
+        } else if (!is_v) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e0 + i < a.rot) y[i] = (float)((Q)v[i] * cs[i][0] + (Q)(a.pairing == 1 ? v[i ^ 1] : o[i]) * cs[i][1]);
         }
-        const float top = row_top<LANES>(v);
-        if (!live || is_q || !there) continue;
-        uint8_t *row = const_cast<uint8_t *>(is_v ? a.c.v : a.c.k) + row_at + head * a.c.rh + (long)lane * Codes<KIND>::bytes;
-        const float scale = store_codes<KIND>(row, v, top);
-        if (lane == 0) const_cast<float *>(is_v ? a.c.vs : a.c.ks)[scale_at + head * a.c.sh] = scale;
+        // (a query's row may be written over itself: its lanes are of one wave, whose loads are done)
+        if (live && is_q) store8<T, VEC>((T *)a.q_out + (long)tok * a.ot + (long)head * a.oh + e0, y);
+        if (base + STEP > Hq) { // rows of keys or values among the block's
+            const float top = row_top<LANES>(y);
+            if (live && !is_q && there) {
+                uint8_t *row = const_cast<uint8_t *>(is_v ? a.c.v : a.c.k) + row_at + head * a.c.rh + (long)lane * Codes<KIND>::bytes;
+                const float scale = store_codes<KIND>(row, y, top);
+                if (lane == 0) const_cast<float *>(is_v ? a.c.vs : a.c.ks)[scale_at + head * a.c.sh] = scale;
+            }
+        }
     }
 }
 

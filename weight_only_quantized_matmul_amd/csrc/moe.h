@@ -57,6 +57,8 @@ struct RouteArgs {
 };
 hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t st);
 
+constexpr int kInlineSlots = 256; // up to as many, the products' blocks find their expert's rows for themselves
+
 // ---------------------------------------------------------------------------
 // A chosen expert: its matrices, how many rows it has, and where their slots t * k + j stand in the order of all slots by expert.
 struct MoeWork {

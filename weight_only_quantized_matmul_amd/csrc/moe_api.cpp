@@ -164,8 +164,7 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
     const bool parts = a.operands >= 4;
     const bool apart = !parts && (a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size));
-    // up to 64 slots every block of the products finds its expert's rows for itself
-    const bool planned = N > 64 || apart || parts;
+    const bool planned = N > wq::kInlineSlots || apart || parts;
     const size_t plan = planned ? (size_t)wq::round_up((N < a.E ? N : a.E) * sizeof(wq::MoeWork), 256) : 0;
     const size_t order = planned ? (size_t)wq::round_up(4 * N, 256) : 0;
     const size_t copy = apart ? (size_t)wq::round_up((long)T * a.xe_n * size, 256) : 0;

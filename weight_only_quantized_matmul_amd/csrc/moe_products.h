@@ -350,7 +350,7 @@ __global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kern
     using P = Products<FMT, GATED, GS, M, WK>;
     __shared__ __align__(16) uint8_t lds[P::LDS];
     __shared__ __align__(16) float red[P::RED / 4];
-    __shared__ int here[64];
+    __shared__ int here[INLINE ? kInlineSlots : 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const MoeShape &sh = GATED ? a.in : a.out;
     const int tiles = (sh.O + P::OUT - 1) / P::OUT, per = GATED ? a.tiles_in : a.tiles_out;
@@ -359,16 +359,27 @@ __global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kern
         return P{a, sh, m0, m1, wave / WK, wave % WK, lane, lane & 15, lane >> 4, lds, red};
     };
     if constexpr (INLINE) {
-        // at most 64 slots: a block a slot, of which the first of an expert works for all of that expert's
-        const int N = a.T * a.k, id = lane < N ? a.ids[lane] : -1;
-        const int e = __builtin_amdgcn_readlane(id, blockIdx.y);
+        // a few slots: a block a slot, of which the first of an expert works for all of that expert's
+        const int N = a.T * a.k;
+        int id[kInlineSlots / 64];
+#pragma unroll
+        for (int q = 0; q < kInlineSlots / 64; ++q) id[q] = 64 * q + lane < N ? a.ids[64 * q + lane] : -1;
+        int mine = id[0];
+#pragma unroll
+        for (int q = 1; q < kInlineSlots / 64; ++q) mine = (int)blockIdx.y >= 64 * q ? id[q] : mine;
+        const int e = __builtin_amdgcn_readlane(mine, blockIdx.y & 63);
         if (e < 0 || e >= a.E) return;
-        const uint64_t same = __ballot(id == e);
-        if (__builtin_ctzll(same) != (int)blockIdx.y) return;
-        const int n = __popcll(same);
+        int n = 0, first = -1;
+#pragma unroll
+        for (int q = 0; q < kInlineSlots / 64; ++q) {
+            const uint64_t same = __ballot(id[q] == e);
+            if (wave == 0 && id[q] == e) here[n + __popcll(same & ((1ull << lane) - 1))] = 64 * q + lane;
+            if (first < 0 && same) first = 64 * q + __builtin_ctzll(same);
+            n += __popcll(same);
+        }
+        if (first != (int)blockIdx.y) return;
         const MoeExpert &ex = a.experts[e];
         P w = work(GATED ? ex.gate : ex.down, GATED ? ex.up : ex.down);
-        if (wave == 0 && id == e) here[__popcll(same & ((1ull << lane) - 1))] = lane;
         __syncthreads();
         for (int s = 0; s < n; s += P::ROWS) w.rows(here + s, min(P::ROWS, n - s), t0, t1);
     } else {

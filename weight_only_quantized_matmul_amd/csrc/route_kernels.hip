@@ -19,8 +19,27 @@ __device__ __forceinline__ uint64_t order(double v) {
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), m) << 32 | (uint32_t)__shfl_xor((int)v, m);
+// The largest code of the wave's lanes, in all of them: within 16 lanes by rotations of rows, then across them.
+template <int N>
+__device__ __forceinline__ uint64_t max_rotated(uint64_t v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), 0x120 + N, 0xF, 0xF, false);
+    const uint64_t o = (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = max_rotated<8>(v);
+    v = max_rotated<4>(v);
+    v = max_rotated<2>(v);
+    v = max_rotated<1>(v);
+    uint64_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 16 * i) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * i);
+        most = o > most ? o : most;
+    }
+    return most;
 }
 
 // NPL: experts a lane
@@ -114,26 +133,18 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const RouteArgs a) {
                 e = i * 64 + lane;
                 pe = p[i];
             }
-        uint64_t most = best;
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) {
-            const uint64_t o = shfl_xor64(most, m);
-            most = o > most ? o : most;
-        }
-        int first = best == most ? e : 1 << 30;
-        const uint64_t ties = __ballot(best == most);
-        if (ties & (ties - 1)) { // several lanes: the lowest expert
-#pragma unroll
-            for (int m = 32; m > 0; m >>= 1) first = min(first, __shfl_xor(first, m));
-        } else {
-            first = __shfl(first, __builtin_ctzll(ties));
-        }
-        pe = __shfl(pe, first & 63);
+        const uint64_t most = wave_max(best);
+        uint64_t ties = __ballot(best == most);
+        int first = __builtin_amdgcn_readlane(e, __builtin_ctzll(ties));
+        for (ties &= ties - 1; ties; ties &= ties - 1) first = min(first, __builtin_amdgcn_readlane(e, __builtin_ctzll(ties))); // the lowest expert
+        const int from = first & 63;
+        pe = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(__builtin_bit_cast(uint64_t, pe) >> 32), from) << 32 |
+                                            (uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint64_t, pe), from));
         if (lane == j) {
             id = first;
             w = pe;
         }
-        if (lane == (first & 63)) {
+        if (lane == from) {
 #pragma unroll
             for (int i = 0; i < NPL; ++i)
                 if (i == first >> 6) key[i] = 0;
