@@ -159,7 +159,9 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     a.ldh = (a.in.O + 3) / 4 * 4;
     a.active = (int)(a.E * (1.0 - std::pow(1.0 - (k < a.E ? k : a.E) / (double)a.E, T)) + 0.5);
     if (a.active < 1) a.active = 1;
-    // operands for the rows that an expert has on average, with room for those that have more
+    // Operands for the rows that an expert has on average, with room for those that have more. 17 tokens on 64 experts of 768 x
+    // 2048 in int4 (2.4 rows) 44.3 us with two, 48.6 with one, 56.3 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
+    // 126 us with eight, 159 with four, 232 with two; one token 34.8 us with one, 36.7 with two.
     const double rows = (double)N / a.active;
     a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
     const bool parts = a.operands >= 4;

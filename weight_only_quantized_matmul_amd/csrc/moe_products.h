@@ -168,6 +168,22 @@ struct Products {
                 for (int u = 0; u < 2; ++u)
                     to[b][u] = __builtin_nontemporal_load((const GLOBAL u32x4 *)((const GLOBAL uint8_t *)matrix(b).w + (woff[b][u] + byte)));
         };
+        // Group scales of a step's halves (units), asked for a step ahead and before the weights that follow: the waits go by the
+        // order of the loads. (Where the registers for them would spill, each when it is needed.)
+        constexpr int SC = GS == 0 ? 1 : TURN ? 2 * UNITS : 2;
+        constexpr bool EARLY = GS != 0 && !BIG && SC <= 4;
+        float sc[2][SC][NT];
+        auto load_sc = [&](float(&to)[SC][NT], int tile, int i) __attribute__((always_inline)) {
+            if constexpr (EARLY) {
+#pragma unroll
+                for (int k = 0; k < SC; ++k) {
+                    const int grp = min(((wk + WK * i) * F::POS + k * (F::POS / SC)) / sh.gs, sh.ng - 1);
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+                        to[k][b] = ((const GLOBAL float *)matrix(b).scales)[(long)grp * sh.O + min(tile * OUT + row0(b) + li, sh.O - 1)];
+                }
+            }
+        };
         // the first phase's activations are asked for ahead of the weights: behind them they would wait for all of those
         Piece ahead[PRE > 0 ? PRE : 1];
 #pragma unroll
@@ -175,6 +191,7 @@ struct Products {
         __builtin_amdgcn_sched_barrier(0);
         aim(t0);
         load_w(w[0], 0);
+        load_sc(sc[0], t0, 0);
         load_w(w[1], 1);
         __builtin_amdgcn_sched_barrier(0);
         __syncthreads(); // the buffer's last readers are done
@@ -203,6 +220,7 @@ struct Products {
                     h[0][b][j] = __builtin_amdgcn_update_dpp(v0, v1, 0x128, 0xF, 0xC, false);
                     h[1][b][j] = __builtin_amdgcn_update_dpp(v1, v0, 0x128, 0xF, 0x3, false);
                 }
+            load_sc(sc[SLOT ^ 1], i + 1 < all ? tile : tile + 1, i + 1 < all ? i + 1 : 0);
             if (i + 2 == all) aim(tile + 1); // the next tile's first steps follow
             load_w(w[SLOT], i + 2 < all ? i + 2 : i + 2 - all);
             i32x4 part[NT][M];
@@ -251,14 +269,16 @@ struct Products {
                             part[b][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[m], q, fresh ? i32x4{0, 0, 0, 0} : part[b][m], 0, 0, 0);
                     }
                     if (last) {
-                        float sc[NT], unit[M];
+                        float unit[M];
 #pragma unroll
                         for (int m = 0; m < M; ++m) unit[m] = units[xunit[m] + at];
-                        if (GS != 0) {
-                            const int pos = (wk + WK * i) * F::POS + half * (F::POS / 2) + (TURN ? 64 * u : 0), grp = min(pos / sh.gs, sh.ng - 1);
+                        constexpr int NOW = EARLY ? SLOT : 0;
+                        const int k = TURN ? half * UNITS + u : half;
+                        if constexpr (GS != 0 && !EARLY) {
+                            const int grp = min(((wk + WK * i) * F::POS + k * (F::POS / SC)) / sh.gs, sh.ng - 1);
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
-                                sc[b] = ((const GLOBAL float *)matrix(b).scales)[(long)grp * sh.O + min(tile * OUT + row0(b) + li, sh.O - 1)];
+                                sc[0][k][b] = ((const GLOBAL float *)matrix(b).scales)[(long)grp * sh.O + min(tile * OUT + row0(b) + li, sh.O - 1)];
                         }
                         // the parts' sums are below 2^24, exact in fp32
 #pragma unroll
@@ -267,7 +287,7 @@ struct Products {
                             for (int m = 0; m < M; ++m) {
                                 const i32x4 &d = part[b][m];
                                 const float v = fmaf(fmaf(fmaf((float)d[3], 256.f, (float)d[2]), 256.f, (float)d[1]), 256.f, (float)d[0]);
-                                acc[b][m] = fmaf(v, GS ? unit[m] * sc[b] : unit[m], acc[b][m]);
+                                acc[b][m] = fmaf(v, GS ? unit[m] * sc[NOW][k][b] : unit[m], acc[b][m]);
                             }
                         if (BIG) __builtin_amdgcn_sched_barrier(0);
                     }
