@@ -595,11 +595,17 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * [T, k] contiguous on the device. An id outside [0, E) adds nothing (a place
  * of a batch without a token, an expert that lives elsewhere); an expert that
  * stands twice counts twice. y may be x or add (same stride).
- * The products are exact in their operands as in wq_matmul_dev (16-bit
- * activations enter as they are, h in full fp32); sums are fp32, the sum over
- * j in the order of j, y rounded once. A token's result does not depend on the
- * other tokens. It uses the stream's workspace as wq_matmul_dev's tiled path
- * does (it may grow, but not while the stream is being captured).
+ * The products take codes as they are, and activations (x, and h in fp32) as
+ * integers of up to 31 bits: whole multiples of a power of two that the 128
+ * (int8 weights), 256 (int4) or 512 (int2) neighbours which meet the same 128
+ * bytes of a row share, each within 2^-30 of the largest magnitude among them
+ * (magnitudes below 2^-96: within 2^-126). Sums over those are exact, sums over
+ * the row fp32, the sum over j fp32 in the order of j, y rounded once. An
+ * infinity or NaN in x, or an h that overflows, makes that expert's row for the
+ * token NaN. What a token gets does not depend on what the other tokens hold
+ * or chose; their number chooses among forms that split the sums differently.
+ * It uses the stream's workspace as wq_matmul_dev's tiled path does (it may
+ * grow, but not while the stream is being captured).
  * For many tokens an expert the grouped calls are faster; T * k above
  * WQ_MOE_MAX_ROWS gives WQ_E_UNSUPPORTED. T == 0 is a no-op.
  */

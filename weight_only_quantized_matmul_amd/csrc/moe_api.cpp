@@ -1,8 +1,6 @@
 // C entry points of the mixture-of-experts operators (include/wqmm.h): argument checks and launches.
-#include <climits>
 #include <cmath>
 #include <new>
-#include <vector>
 
 #include "entry.h"
 #include "moe.h"

@@ -2,12 +2,21 @@
 //
 //     y[t] = add[t] + sum_j weights[t,j] * down_e . (silu(gate_e . x[t]) * (up_e . x[t])),  e = ids[t,j]
 //
-// Which expert works on which rows is known on the device only. A first
-// kernel sorts the slots t * k + j by expert and lays the activations out; then
-// the products of gate and up, with the activation as their epilogue, write h;
-// the products of down write one row a slot; and the last kernel adds each
-// token's rows in the order of its slots, so results do not depend on what
-// else the batch holds.
+// Which expert works on which rows is known on the device only. Up to
+// kInlineSlots slots t * k + j the products' blocks find their expert's slots
+// themselves. For more, and where the activations have to be laid out first, a
+// kernel of its own sorts the slots by expert (a counting sort in one block)
+// and makes the activations' parts, or a copy whose rows can be read four
+// elements at a time. The products of gate and up, with the activation as their
+// epilogue, write h; the products of down write one row a slot; and the last
+// kernel adds each token's rows in the order of its slots, so results do not
+// depend on what else the batch holds. (Products that add into y themselves
+// would need atomics, whose order changes results.)
+//
+// What these two kernels take is mostly their launch and one pass through
+// memory's latency: 4.0 us for the sum of one token's 8 rows of 6144, 5.8 us for
+// the plan and parts of 64 tokens of 6144, 17 tokens on 64 experts without a
+// plan 44.4 us, with one 46.6 us.
 #include "moe_parts.h"
 
 namespace wq {

@@ -4,7 +4,12 @@
 // as 16 * q, int2 as 64 * q), where bf16 ones took two instructions each and bound the vector units. An activation becomes a
 // 31-bit integer, in units of a power of two that the activations of a step (the 128 bytes of a row of weights that they
 // meet: 128, 256 or 512 of them) share, and that as four signed base-256 digits, its parts: x = unit * sum_p d_p 256^p within
-// 2^-31 of the step's largest magnitude. The integer sums are exact; each step's goes to the fp32 sum with its unit.
+// 2^-30 of the step's largest magnitude. The integer sums are exact; each step's goes to the fp32 sum with its unit.
+//
+// With a few rows an expert the weights' stream bounds them, read once at up to 4.8 TB/s (a large copy's rate): one token on 8
+// experts of 2048 x 6144 in int4, 151 MB, 20.2 us (gate and up: 4.9 TB/s) and 12.8 us (down: 3.9 TB/s). Loads of the next two
+// steps are always in flight, across tiles too. With more rows reading the operands from LDS bounds them, 16 stacked rows a
+// KiB: 64 tokens on 8 experts of the same shape in int8, 302 MB, 66.8 and 42.6 us (2.8 TB/s), 126 us with all launches.
 #pragma once
 
 #include <type_traits>
