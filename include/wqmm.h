@@ -607,7 +607,8 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * It uses the stream's workspace as wq_matmul_dev's tiled path does (it may
  * grow, but not while the stream is being captured).
  * For many tokens an expert the grouped calls are faster; T * k above
- * WQ_MOE_MAX_ROWS gives WQ_E_UNSUPPORTED. T == 0 is a no-op.
+ * WQ_MOE_MAX_ROWS, or shapes whose launches could have 2^32 threads (16 * F, 8 *
+ * D_out times min(E, T * k)), give WQ_E_UNSUPPORTED. T == 0 is a no-op.
  */
 int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
                    int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream);

@@ -227,6 +227,32 @@ def test_append_rope_equals_its_parts_and_runs_in_a_graph():
         assert ((out[0] - out[2]).abs() <= 1.001 * step_).all()  # a code at a border may fall to either side
 
 
+def test_append_rope_more_tokens_than_a_launch_has_threads():
+    """A prompt of 2^24 + 9 tokens (a block of 256 threads each): its last tokens as a batch of their own leaves them."""
+    T, last, page, D = (1 << 24) + 9, 40, 128, 64
+    gu.banner("append_rope T=%d" % T)
+    pages = -(-T // page)
+    g = torch.Generator("cuda").manual_seed(4)
+    k, v = (torch.zeros((T, 1, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    for t in (k, v):
+        t[:last].normal_(generator=g)
+        t[-last:].normal_(generator=g)
+    rope = wq.wq_rope_create(D, 0, 1e6, [D // 2])
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    caches = []
+    for n in range(2):
+        pools = [torch.zeros((pages, 1, page, D // 2), dtype=torch.uint8, device="cuda") for _ in "kv"]
+        caches.append((wq.KvCache(wq.WQ_KV_I4, *pools, *[torch.zeros((pages, 1, page), device="cuda") for _ in "kv"]), pools))
+    for (cache, _), lo in zip(caches, (0, T - last)):
+        batch = wq.KvBatch(torch.tensor([0, T - lo], dtype=torch.int32, device="cuda"), torch.tensor([T], dtype=torch.int32, device="cuda"), table, T - lo)
+        wq.wq_kv_append_rope_dev(cache, batch, rope, k[lo:], v[lo:])
+    torch.cuda.synchronize()
+    for whole, part in zip(caches[0][1], caches[1][1]):
+        whole, part = (p.view(-1, D // 2)[:T] for p in (whole, part))
+        assert torch.equal(whole[-last:], part[-last:]) and not torch.equal(whole[:last], part[:last])
+    wq.wq_rope_free(rope)
+
+
 def test_append_rope_refusals_of_the_binding():
     rng = np.random.default_rng(9)
     c = Case(rng, dref.I8, "f32", 64, 2, [3], [3], 4)

@@ -89,6 +89,15 @@ def test_route_strides_and_nothing():
     wq.wq_moe_route_dev(big[:0, :64], torch.empty((0, 4), dtype=torch.int32, device="cuda"), torch.empty((0, 4), device="cuda"))
 
 
+def test_route_more_tokens_than_a_launch_has_threads():
+    T = (1 << 32) // 64 + 7  # a wave a token
+    ids, w = torch.full((T, 1), -77, dtype=torch.int32, device="cuda"), torch.zeros((T, 1), device="cuda")
+    gu.banner("route (%d, 1)" % T)
+    wq.wq_moe_route_dev(torch.ones((T, 1), dtype=torch.bfloat16, device="cuda"), ids, w, scale=0.5)
+    torch.cuda.synchronize()
+    assert int(ids.abs().max()) == 0 and float(w.min()) == 0.5 and float(w.max()) == 0.5
+
+
 def test_route_refusals_of_the_binding():
     s = torch.zeros((2, 8), device="cuda")
     ids, w = torch.empty((2, 4), dtype=torch.int32, device="cuda"), torch.empty((2, 4), device="cuda")
@@ -324,6 +333,17 @@ def test_moe_refusals():
             wq.wq_moe_ffn_dev(a.moe, *args)
     with pytest.raises(ValueError):
         wq.wq_moe_ffn_dev(a.moe, x, ids, w, x, add=x.to(torch.bfloat16))
+    # one tensor of 2^18 + 16 rows as each of 1024 experts: the products' blocks could have 2^32 threads
+    F, zeros = (1 << 18) + 16, np.zeros
+    wide = [wq.wq_tensor_upload(None, 0, wq.WQ_I2, rows, cols, zeros(rows * cols // 4, dtype=np.uint8), zeros(rows, dtype=np.float32)) for rows, cols in ((F, 16), (16, F))]
+    many = wq.wq_moe_create([wide[0]] * 1024, [wide[0]] * 1024, [wide[1]] * 1024)
+    y = torch.zeros((1024, 16), device="cuda")
+    with pytest.raises(wq.WqError) as e:
+        wq.wq_moe_ffn_dev(many, y, torch.zeros((1024, 1), dtype=torch.int32, device="cuda"), torch.zeros((1024, 1), device="cuda"), y)
+    assert e.value.code == wq.WQ_E_UNSUPPORTED
+    wq.wq_moe_free(many)
+    for t in wide:
+        wq.wq_tensor_free(t)
     gu.reinit_with_env(WQ_FAULT="launch")
     for call in (lambda: wq.wq_moe_ffn_dev(a.moe, x, ids, w, x), lambda: wq.wq_moe_route_dev(x, ids, w)):
         with pytest.raises(wq.WqError) as e:
@@ -390,6 +410,29 @@ def test_route_and_moe_in_a_graph(T):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (ids, w, y)))
     layer.free()
+
+
+@pytest.mark.parametrize("T,D,k", [(2, 256, 2), (9, 250, 3), (64, 256, 6), (90, 258, 3), (70, 256, 1)])
+@pytest.mark.parametrize("fmt,gs", [(ref.I4, 0), (ref.I8, 64), (ref.I2, 0)])
+def test_moe_calls_with_nothing_between(T, D, k, fmt, gs):
+    """Two layers in turn on one stream leave each other's results, and their own inputs, as they are."""
+    rng = np.random.default_rng(15)
+    states = []
+    for n in range(2):
+        layer = Layer(rng, fmt, 70 + 3 * n, D, 100, gs=gs)
+        ids, w = choose(rng, T, layer.E, k)
+        x, add = rand(rng, (T, D), "f32"), rand(rng, (T, D), "f32")
+        states.append((layer, x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), add, add.clone(), check_moe(layer, x, ids, w, "f32", add=add)))
+    outs = []
+    for n in (0, 1, 0, 0, 1):
+        layer, x, ids, w, add, _, _ = states[n]
+        outs.append((n, torch.empty_like(x)))
+        wq.wq_moe_ffn_dev(layer.moe, x, ids, w, outs[-1][1], add=add)
+    torch.cuda.synchronize()
+    for n, y in outs:
+        assert torch.equal(y, states[n][6]) and torch.equal(states[n][4], states[n][5])
+    for s in states:
+        s[0].free()
 
 
 def test_moe_capture_needs_a_workspace():

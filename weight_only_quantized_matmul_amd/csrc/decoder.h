@@ -104,6 +104,7 @@ struct KvRopeArgs {
     int H, rot, pairing;
     double turns[WQ_ROPE_MAX_ROT / 2];
     uint8_t axis[WQ_ROPE_MAX_ROT / 2];
+    int first; // of the launch's tokens
 };
 hipError_t launch_kv_append_rope(const KvRopeArgs &a, int kind, int dim, int dtype, bool vec, int cus, hipStream_t st);
 

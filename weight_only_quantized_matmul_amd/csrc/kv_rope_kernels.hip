@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_rope_kernel(const KvRopeAr
     __shared__ double2 trig[WQ_ROPE_MAX_ROT / 2];
     __shared__ long found; // sequence << 32 | position, or -1
     const int tid = threadIdx.x, lane = tid & (LANES - 1), half = a.rot / 2;
-    const int tok = blockIdx.x;
+    const int tok = a.first + (int)blockIdx.x;
     const int Hq = a.q ? a.H : 0, rows = Hq + 2 * a.c.heads;
     const int r0 = (int)((long)rows * blockIdx.y / gridDim.y), r1 = (int)((long)rows * (blockIdx.y + 1) / gridDim.y);
     // a row's 8 elements and those that they turn with (asked for a round ahead, 2436 tokens took 43 us, with the read, instead of 36)
@@ -129,14 +129,19 @@ hipError_t launch_d(const KvRopeArgs &a, bool vec, int cus, hipStream_t st) {
     const long rows = (a.q ? a.H : 0) + 2L * a.c.heads, most = (rows * (D / 8) + kThreads - 1) / kThreads;
     long gy = a.b.T >= 2 * cus ? 1 : (2 * cus + a.b.T - 1) / a.b.T;
     gy = gy < most ? gy : most;
-    const long piece = kMaxThreads / kThreads; // tokens a launch: all that an int counts fit in one
-    if (a.b.T > piece) return hipErrorNotSupported;
-    const dim3 grid((unsigned)a.b.T, (unsigned)gy), block(kThreads);
-    if (vec)
-        hipLaunchKernelGGL((kv_append_rope_kernel<T, KIND, D, true>), grid, block, 0, st, a);
-    else
-        hipLaunchKernelGGL((kv_append_rope_kernel<T, KIND, D, false>), grid, block, 0, st, a);
-    return hipGetLastError();
+    const long piece = kMaxThreads / kThreads / gy; // tokens a launch
+    for (long done = 0; done < a.b.T; done += piece) {
+        KvRopeArgs b = a;
+        b.first = (int)done;
+        const dim3 grid((unsigned)(a.b.T - done < piece ? a.b.T - done : piece), (unsigned)gy), block(kThreads);
+        if (vec)
+            hipLaunchKernelGGL((kv_append_rope_kernel<T, KIND, D, true>), grid, block, 0, st, b);
+        else
+            hipLaunchKernelGGL((kv_append_rope_kernel<T, KIND, D, false>), grid, block, 0, st, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <typename T, int KIND>

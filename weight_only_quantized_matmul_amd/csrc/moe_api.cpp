@@ -161,6 +161,11 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     // 2048 in int4 (2.4 rows) 44.3 us with two, 48.6 with one, 56.3 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
     // 126 us with eight, 159 with four, 232 with two; one token 34.8 us with one, 36.7 with two.
     const double rows = (double)N / a.active;
+    // (of the products' blocks, of 256 threads, as many as their smallest tiles of outputs make)
+    const double pairs = N <= wq::kInlineSlots || N < a.E ? N : a.E;
+    if ((double)T * (a.out.O + 255.0) > wq::kMaxThreads || (double)N * a.out.kp / 16 > wq::kMaxThreads ||
+        pairs * (a.in.O + 15.0) * 16 > wq::kMaxThreads || pairs * (a.out.O + 31.0) * 8 > wq::kMaxThreads)
+        return WQ_E_UNSUPPORTED;
     a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
     const bool parts = a.operands >= 4;
     const bool apart = !parts && (a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size));

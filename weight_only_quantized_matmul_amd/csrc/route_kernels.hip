@@ -170,16 +170,30 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const RouteArgs a) {
 
 template <typename T>
 hipError_t launch_t(const RouteArgs &a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.T + (long)kWaves - 1) / kWaves)), block(64 * kWaves);
+    const dim3 block(64 * kWaves);
     const size_t lds = a.groups > 1 ? sizeof(double) * kWaves * a.E : 0;
-#define WQ_ROUTE(N)                                                                                                    \
-    if (a.E <= 64 * N) {                                                                                               \
-        hipLaunchKernelGGL((route_kernel<T, N>), grid, block, lds, st, a);                                             \
-        return hipGetLastError();                                                                                      \
+    const int piece = (int)(kMaxThreads / 64) / kWaves * kWaves; // tokens a launch
+    for (long done = 0; done < a.T; done += piece) {
+        RouteArgs b = a;
+        b.scores = (const T *)a.scores + done * a.stride;
+        b.ids = a.ids + done * a.k;
+        b.weights = a.weights + done * a.k;
+        b.T = (int)(a.T - done < piece ? a.T - done : piece);
+        const dim3 grid((unsigned)((b.T + kWaves - 1) / kWaves));
+        if (a.E <= 64)
+            hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, lds, st, b);
+        else if (a.E <= 128)
+            hipLaunchKernelGGL((route_kernel<T, 2>), grid, block, lds, st, b);
+        else if (a.E <= 256)
+            hipLaunchKernelGGL((route_kernel<T, 4>), grid, block, lds, st, b);
+        else if (a.E <= 512)
+            hipLaunchKernelGGL((route_kernel<T, 8>), grid, block, lds, st, b);
+        else
+            hipLaunchKernelGGL((route_kernel<T, 16>), grid, block, lds, st, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    WQ_ROUTE(1) WQ_ROUTE(2) WQ_ROUTE(4) WQ_ROUTE(8) WQ_ROUTE(16)
-#undef WQ_ROUTE
-    return hipErrorInvalidValue;
+    return hipSuccess;
 }
 
 } // namespace
