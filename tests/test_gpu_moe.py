@@ -437,15 +437,16 @@ def test_moe_calls_with_nothing_between(T, D, k, fmt, gs):
 
 def test_moe_capture_needs_a_workspace():
     rng = np.random.default_rng(14)
-    layer = Layer(rng, ref.I4, 2, 4096, 64)
-    T = 8000
-    x = torch.zeros((T, 4096), device="cuda")
+    # 4 GiB for the experts' rows alone: more than any stream's workspace, which a captured call could use instead, has grown to
+    layer = Layer(rng, ref.I4, 2, 64, 64, O=1 << 16)
+    T = wq.WQ_MOE_MAX_ROWS // 2
+    x, y = torch.zeros((T, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((T, 1 << 16), dtype=torch.bfloat16, device="cuda")
     ids, w = torch.zeros((T, 2), dtype=torch.int32, device="cuda"), torch.zeros((T, 2), device="cuda")
     side, codes = torch.cuda.Stream(), []
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=side):
         try:
-            wq.wq_moe_ffn_dev(layer.moe, x, ids, w, x, stream=side)
+            wq.wq_moe_ffn_dev(layer.moe, x, ids, w, y, stream=side)
         except wq.WqError as e:
             codes.append(e.code)
         torch.zeros(1, device="cuda")
