@@ -14,8 +14,11 @@ template <int FMT>
 struct Fmt {
     static constexpr int EPB = FMT == WQ_I8 ? 1 : FMT == WQ_I4 ? 2 : 4;
     static constexpr int POS = 128 * EPB; // positions of a step
-    static constexpr float UNSCALE = FMT == WQ_I8 ? 1.0f : FMT == WQ_I4 ? 0.0625f : 0.015625f;
+    // Units take off what the codes are multiplied by, and 2^16 that the sums give back (kBack): a step's activations times codes
+    // can be 2^14 times the largest activation, and their sum stays finite like it.
+    static constexpr float UNSCALE = (FMT == WQ_I8 ? 1.0f : FMT == WQ_I4 ? 0x1p-4f : 0x1p-6f) * 0x1p-16f;
 };
+constexpr float kBack = 0x1p16f;
 
 // Bytes of b where sel's are 0..3, of a where 4..7.
 __device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t sel) { return __builtin_amdgcn_perm(a, b, sel); }
@@ -33,7 +36,7 @@ __device__ __forceinline__ float make_parts(const float (&x)[16], u32x4 (&part)[
     for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int m = F::POS / kPiece / 2; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    // 2^(e + 1) is above it, and the unit 2^(e - 29) a normal number
+    // 2^(e + 1) is above it; 2^(e - 29) and its inverse are normal numbers, and the unit, at least 2^-147, is exact
     const int e = min(max((int)(top >> 23) - 127, -96), 127);
     const bool bad = top >= 0x7F800000u;
     const float up = __uint_as_float((uint32_t)(127 + 29 - e) << 23); // 2^(29 - e)

@@ -287,14 +287,15 @@ struct Products {
                             for (int b = 0; b < NT; ++b)
                                 sc[0][k][b] = ((const GLOBAL float *)matrix(b).scales)[(long)grp * sh.O + min(tile * OUT + row0(b) + li, sh.O - 1)];
                         }
-                        // the parts' sums are below 2^24, exact in fp32
+                        // The parts' sums are below 2^24, exact in fp32. A step's sum meets its unit first and a group's scale
+                        // after: a unit times a scale could be too small to keep its bits where the product of all three is not.
 #pragma unroll
                         for (int b = 0; b < NT; ++b)
 #pragma unroll
                             for (int m = 0; m < M; ++m) {
                                 const i32x4 &d = part[b][m];
                                 const float v = fmaf(fmaf(fmaf((float)d[3], 256.f, (float)d[2]), 256.f, (float)d[1]), 256.f, (float)d[0]);
-                                acc[b][m] = fmaf(v, GS ? unit[m] * sc[NOW][k][b] : unit[m], acc[b][m]);
+                                acc[b][m] = GS ? fmaf(v * unit[m], sc[NOW][k][b], acc[b][m]) : fmaf(v, unit[m], acc[b][m]);
                             }
                         if (BIG) __builtin_amdgcn_sched_barrier(0);
                     }
@@ -354,7 +355,9 @@ struct Products {
                     float v = 0.f;
 #pragma unroll
                     for (int q = 0; q < WK; ++q) v += red[((grp * WK + q) * NT + b) * 64 + 16 * s + (c & 15)];
-                    return GS ? v : v * ((const GLOBAL float *)matrix(b).scales)[o];
+                    if constexpr (GS) return v * kBack; // (what was lost below the smallest number is below 2^-133 here)
+                    const float s_ = ((const GLOBAL float *)matrix(b).scales)[o];
+                    return fabsf(v) < 1.f ? v * kBack * s_ : v * (s_ * kBack);
                 };
                 const int slot = slots[4 * m + s];
                 if constexpr (GATED) {
