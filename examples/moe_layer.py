@@ -79,8 +79,9 @@ class MoeLayer:
         wq.wq_rmsnorm_block_dev(b["a"], x, self.eps, w_post=self.w[1], alpha=self.alpha, w_pre=self.w[2], y=b["y"], sum_out=b["mid"], **s)
         wq.wq_matmul_dev(self.router, b["y"], b["scores"], **s)
         wq.wq_moe_route_dev(b["scores"], b["chosen"], b["share"], bias=self.bias, gating=wq.WQ_GATE_SIGMOID, groups=4, top_groups=2, **s)
-        b["ids"][:, :self.k].copy_(b["chosen"])
-        b["weights"][:, :self.k].copy_(b["share"])
+        with torch.cuda.stream(stream):  # torch's copies belong between the choice and the experts (None: the current stream)
+            b["ids"][:, :self.k].copy_(b["chosen"])
+            b["weights"][:, :self.k].copy_(b["share"])
         wq.wq_moe_ffn_dev(self.moe, b["y"], b["ids"], b["weights"], b["f"], **s)
         wq.wq_rmsnorm_block_dev(b["f"], b["mid"], self.eps, alpha=self.alpha, w_pre=self.w[3], y=b["next"], sum_out=b["stream"], **s)
 

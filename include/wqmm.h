@@ -600,7 +600,7 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * (int8 weights), 256 (int4) or 512 (int2) neighbours which meet the same 128
  * bytes of a row share, each within 2^-30 of the largest magnitude among them
  * (magnitudes below 2^-96: within 2^-126). Sums over those are exact, sums over
- * the row fp32 (with group scales also what 2^-126 is off), the sum over j
+ * the row fp32 (with group scales within 2^-126 besides), the sum over j
  * fp32 in the order of j, y rounded once. An
  * infinity or NaN in x, or an h that overflows, makes that expert's row for the
  * token NaN. What a token gets does not depend on what the other tokens hold
