@@ -193,9 +193,10 @@ int wq_matmul_t(const wq_tensor *t, const float *x, int S, float *y);
  * A graph keeps the buffer that its calls were captured with: that buffer
  * is never freed and never passes to another stream, whatever calls follow
  * (a stream that needs more gets a new one and leaves the old one, until
- * the process ends, to the graph). The stream it was captured from goes on
- * with the buffer until then, so do not replay the graph while that stream,
- * or another graph with the same buffer, runs calls that use a workspace.
+ * the process ends, to the graph). The stream whose workspace it was (the one
+ * captured, or the one that lent the largest) goes on with the buffer until
+ * then, so do not replay the graph while that stream, or another graph with
+ * the same buffer, runs calls that use a workspace: results would be wrong.
  */
 int wq_matmul_dev(const wq_tensor *t, const float *x_dev, int S, float *y_dev, void *hip_stream);
 

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "decoder.h"
+#include "moe_plan.h"
 #include "wq_internal.h"
 
 namespace wq {
@@ -60,13 +61,6 @@ hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t st);
 constexpr int kInlineSlots = 256; // up to as many, the products' blocks find their expert's rows for themselves
 
 // ---------------------------------------------------------------------------
-// A chosen expert: its matrices, how many rows it has, and where their slots t * k + j stand in the order of all slots by expert.
-struct MoeWork {
-    MoeExpert e;
-    int rows, first;
-    int pad[2];
-};
-
 struct MoeArgs {
     const MoeExpert *experts;
     int E, T, k, cus;

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kPrepThreads) void moe_prepare_kernel(const MoeArgs
             at[e] = run & 0xFFFF;
             if (n) {
                 MoeWork &w = a.plan[run >> 16];
-                w.e = a.experts[e];
+                w.expert = e;
                 w.rows = n;
                 w.first = run & 0xFFFF;
                 run += 0x10000u + n;

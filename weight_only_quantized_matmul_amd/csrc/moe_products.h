@@ -413,15 +413,27 @@ __global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kern
         __syncthreads();
         for (int s = 0; s < n; s += P::ROWS) w.rows(here + s, min(P::ROWS, n - s), t0, t1);
     } else {
-        const MoeWork &k = a.plan[blockIdx.y];
-        const int n = k.rows;
+        // every wave reads the plan, for its expert's matrices; the rows are those that the first one read
+        __shared__ int span[2];
+        const int N = a.T * a.k;
+        MoeWork raw = a.plan[blockIdx.y];
+        asm("" : "+s"(raw.expert), "+s"(raw.rows), "+s"(raw.first)); // (read once: what is checked is what is used)
+        const MoeWork k = bounded(raw, a.E, N);
+        const MoeExpert &ex = a.experts[k.expert];
+        const MoeMatrix m0 = GATED ? ex.gate : ex.down, m1 = GATED ? ex.up : ex.down; // (scalar loads, ahead of the barrier)
+        if (threadIdx.x == 0) {
+            span[0] = k.rows;
+            span[1] = k.first;
+        }
+        __syncthreads();
+        const int n = __builtin_amdgcn_readfirstlane(span[0]);
         if (n == 0) return;
-        P w = work(GATED ? k.e.gate : k.e.down, GATED ? k.e.up : k.e.down);
-        const int *slots = a.order + k.first;
+        P w = work(m0, m1);
+        const int *slots = a.order + __builtin_amdgcn_readfirstlane(span[1]);
         for (int s = 0; s < n; s += P::ROWS) {
             const int some = min(P::ROWS, n - s);
-            __syncthreads(); // the last rows' readers are done
-            if (threadIdx.x < some) here[threadIdx.x] = slots[s + threadIdx.x];
+            if (s > 0) __syncthreads(); // the last rows' readers are done
+            if (threadIdx.x < some) here[threadIdx.x] = bounded_slot(slots[s + threadIdx.x], N);
             __syncthreads();
             w.rows(here, some, t0, t1);
         }
