@@ -615,6 +615,19 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
 int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
                    int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream);
 
+/*
+ * The plan of wq_moe_ffn_dev for these sizes as text (host only; buffers are
+ * not looked at, x counts as aligned, 256 CUs where the device is not open), for
+ * tests and logs: "in operands=2 waves=1 tiles=3 rows=8 phases=1-2 out ...
+ * plan=0 copy=0 workspace=...". For gate and up (in) and for down (out): operands
+ * of four activations, waves along a row of weights, tiles of outputs a block
+ * takes one after another, rows of an expert at a time, and the phases in which
+ * a block takes the activations of one row and of all of those; plan: a launch
+ * sorts the slots by expert; copy: x is copied into aligned rows; and the
+ * workspace in bytes.
+ */
+int wq_describe_moe(const wq_moe *moe, int dtype, int T, int k, long x_stride, char *buf, size_t buflen);
+
 #ifdef __cplusplus
 }
 #endif

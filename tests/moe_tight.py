@@ -86,3 +86,42 @@ def moe(x, ids, w, experts, add=None):
     terms = np.abs(v * wj).sum(1) + (0 if add is None else np.abs(add))
     bound = (b * np.abs(wj)).sum(1)
     return y, bound + (k + 1) * U * (terms + bound)
+
+
+def pack(codes, fmt):
+    """uint8 [rows, row bytes] of whole codes [rows, cols]."""
+    per = 8 // BITS[fmt]
+    q = (codes + (0 if fmt == I8 else 2 ** (BITS[fmt] - 1))).astype(np.int64) & (2 ** BITS[fmt] - 1)
+    q = np.pad(q, ((0, 0), (0, -q.shape[1] % per)))
+    return sum(q[:, i::per] << (BITS[fmt] * i) for i in range(per)).astype(np.uint8)
+
+
+COLS = 120  # of the rows below: one step of any format, in two groups of 64
+PAIRS = [(g + 2 * i + 1, g + 2 * i + 2) for g in (0, 64) for i in range(10)]  # columns that cancel, in one group
+SMALL = [c for c in range(1, COLS) if c not in sum(PAIRS, ())]
+
+
+def cancelling_rows(rng, T):
+    """float32 [T, COLS]: 1 in column 0, ones of both signs in PAIRS and in SMALL numbers of one base-256 digit in units of 2^-29,
+    the lowest in token 0, the next in token 1, the third in token 2, two of them in token 3, and so on."""
+    x = np.zeros((T, COLS))
+    x[:, 0] = 1
+    for t in range(T):
+        for i, j in PAIRS:
+            x[t, i] = rng.choice([-1, 1])
+            x[t, j] = -x[t, i]
+        m = rng.integers(1, 128, len(SMALL)) * rng.choice([-1, 1], len(SMALL)) * 256.0 ** (t % 4 % 3)
+        if t % 4 == 3:
+            m += rng.integers(-128, 128, len(SMALL)) * 256.0
+        x[t, SMALL] = m * 2.0 ** -29
+    return x.astype(np.float32)
+
+
+def cancelling_codes(rng, rows, fmt):
+    """Codes [rows, COLS]: none in column 0, equal ones in a pair's columns, any in SMALL."""
+    top = 2 ** (BITS[fmt] - 1)
+    q = rng.integers(-top, top, (rows, COLS))
+    q[:, 0] = 0
+    for i, j in PAIRS:
+        q[:, i] = q[:, j]
+    return q

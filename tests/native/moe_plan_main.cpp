@@ -2,6 +2,7 @@
 // checks and exits with their number.
 #include <climits>
 #include <cstdio>
+#include <initializer_list>
 #include <random>
 #include <type_traits>
 
@@ -54,11 +55,49 @@ void good_plans_stay() {
     }
 }
 
+void phases_fit_their_buffer() {
+    for (int m : {1, 2, 3, 4, 8})
+        for (int wk : {1, 2, 4})
+            for (int pos : {128, 256, 512}) {
+                const int rows = wq::moe_rows(m, wk, pos);
+                CHECK(rows >= 1 && rows <= 4 * m && rows <= 64);
+                for (int n = 1; n <= rows; ++n)
+                    for (int steps : {1, 2, 3, 4, 5, 15, 16, 17, 48, 1000, 1 << 21}) {
+                        const int all = wq::moe_steps(steps, wk), per = wq::moe_phase(m, wk, pos, n, all);
+                        CHECK(all % 2 == 0 && all * wk >= steps && (all - 2) * wk < steps);
+                        CHECK(per >= 2 && per % 2 == 0 && per <= all);
+                        // parts in rows of 16 bytes more than their positions, and a unit a step
+                        CHECK((long)n * 4 * (per * wk * pos + 16) + (long)n * per * wk * 4 <= wq::moe_lds(m));
+                        const long pieces = (long)n * per * wk * pos / wq::kMoePiece; // counted by 32-bit reciprocals
+                        CHECK(pieces < 65536);
+                    }
+            }
+}
+
+void forms() {
+    for (int gated = 0; gated < 2; ++gated)
+        for (int O : {1, 16, 17, 127, 1610, 3300, 65536, 1 << 22})
+            for (int steps : {1, 3, 4, 15, 16, 1000})
+                for (int ops : {1, 2, 4, 8})
+                    for (int active : {1, 3, 64, 1024})
+                        for (int turned = 0; turned < 2; ++turned) {
+                            const wq::MoeForm f = wq::moe_form(gated, O, steps, turned, ops, active, 256);
+                            const int out = wq::moe_outputs(gated, f.wk), tiles = (O + out - 1) / out;
+                            CHECK(f.m == (turned && ops >= 4 ? 3 : ops) && (f.wk == 1 || f.wk == 2 || f.wk == 4));
+                            CHECK(f.tiles >= 1 && f.tiles <= tiles && (f.tiles == 1 || !wq::moe_big(f.m)));
+                        }
+    // one token, 8 of 16 experts of 2048 x 6144 in int4; 64 tokens on 256 such experts
+    const wq::MoeForm one = wq::moe_form(true, 2048, 24, false, 1, 8, 256), many = wq::moe_form(true, 2048, 24, false, 1, 222, 256);
+    CHECK(one.m == 1 && one.wk == 2 && one.tiles == 1 && many.wk == 1 && many.tiles == 9);
+}
+
 } // namespace
 
 int main() {
     any_contents();
     good_plans_stay();
+    phases_fit_their_buffer();
+    forms();
     if (failures == 0) std::printf("all checks passed\n");
     return failures;
 }

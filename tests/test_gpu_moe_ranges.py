@@ -16,6 +16,8 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU hosts
 import gpu_util as gu  # noqa: E402
 import weight_only_quantized_matmul_amd as wq  # noqa: E402
 
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
 
 @pytest.fixture(autouse=True)
 def _init():
@@ -36,14 +38,17 @@ class Layer:
         self.experts = [mats[e % len(mats)] for e in range(E)]
         self.moe = wq.wq_moe_create(*([self.handles[e % len(mats)][n] for e in range(E)] for n in range(3)))
 
-    def check(self, x, ids, w, what=""):
-        """x float32 [T, D] numpy, ids, w numpy; the worst error over its bound."""
-        gu.banner("moe %s T=%d k=%d E=%d" % (what, x.shape[0], ids.shape[1], len(self.experts)))
-        y = torch.full((x.shape[0], self.moe.D_out), 7.0, device="cuda")
-        wq.wq_moe_ffn_dev(self.moe, torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), y)
+    def check(self, x, ids, w, what="", dtype="f32", apart=False):
+        """x float32 [T, D] numpy, taken in dtype (apart: in rows of odd stride), ids, w numpy: the result, which is within its bound."""
+        gu.banner("moe %s T=%d k=%d E=%d D=%d F=%d %s" % (what, x.shape[0], ids.shape[1], len(self.experts), self.moe.D, self.moe.F, dtype))
+        x = torch.from_numpy(x).cuda().to(DT[dtype])
+        if apart:
+            x = torch.cat([x, x[:, :1 + x.shape[1] % 2]], 1)[:, :x.shape[1]]
+        y = torch.full((x.shape[0], self.moe.D_out), 7.0, dtype=x.dtype, device="cuda")
+        wq.wq_moe_ffn_dev(self.moe, x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), y)
         torch.cuda.synchronize()
-        want, bound = tight.moe(x.astype(np.float64), ids, w, self.experts)
-        bound = bound + tight.U * (np.abs(want) + bound) + 2.0 ** -149
+        want, bound = tight.moe(x.double().cpu().numpy(), ids, w, self.experts)
+        bound = bound + ref.HALF[dtype] * (np.abs(want) + bound) + ref.TINY[dtype]
         worst = (np.abs(y.double().cpu().numpy() - want) / bound).max()
         assert worst <= 1, "%s: worst err/bound %.3g" % (what, worst)
         return y
@@ -100,3 +105,35 @@ def test_moe_rows_that_are_not_finite(fmt, gs, T):
     torch.cuda.synchronize()
     assert not torch.isfinite(y[[0, T - 1]]).any() and torch.equal(y[1:T - 1], clean[1:T - 1])
     layer.free()
+
+
+@pytest.mark.parametrize("fmt,gs", [(ref.I8, 0), (ref.I8, 64), (ref.I4, 0), (ref.I4, 64), (ref.I2, 0), (ref.I2, 64)])
+@pytest.mark.parametrize("T", [3, 8, 14, 40])  # one, two, four and eight operands
+def test_moe_every_digit_counts(fmt, gs, T):
+    """Large activations cancel and the result is that of small ones, of one base-256 digit each. Gate's only code makes z = 64,
+    whose silu is 64 exactly. First the product with up is such a one, then, with up the identity (h = 64 x exactly), down's."""
+    rng = np.random.default_rng(33)
+    n = tight.COLS
+    one = lambda codes, scale: tight.Matrix(tight.pack(codes, fmt), np.full((n, 2) if gs else n, scale, np.float32), n, fmt, gs)  # noqa: E731
+    first, eye = np.zeros((n, n), np.int64), np.eye(n, dtype=np.int64)
+    first[:, 0] = 1
+    scales = (2.0 ** rng.integers(-3, 4, (n, 2) if gs else n)).astype(np.float32)
+    codes = [tight.cancelling_codes(rng, n, fmt) for _ in range(2)]
+    mixed = [tight.Matrix(tight.pack(q, fmt), scales, n, fmt, gs) for q in codes]
+    x = tight.cancelling_rows(rng, T)
+    ids, w = (np.arange(T, dtype=np.int32) % 2)[:, None], np.ones((T, 1), np.float32)
+    for up, down in (([m for m in mixed], [one(eye, 1)] * 2), ([one(eye, 1)] * 2, mixed)):
+        layer = Layer([[one(first, 64), u, d] for u, d in zip(up, down)])
+        gu.banner("digits fmt %d gs %d T=%d" % (fmt, gs, T))
+        y = torch.empty((T, n), device="cuda")
+        wq.wq_moe_ffn_dev(layer.moe, torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), y)
+        torch.cuda.synchronize()
+        for t in range(T):
+            x64 = x[t:t + 1].astype(np.float64)
+            u, Eu = up[t % 2].product(x64, np.zeros((1, n))) if down is not mixed else (x64, np.zeros((1, n)))
+            # 64 u is exact in fp32; y passes one sum over its only expert, without rounding, and its own type, fp32
+            want, bound = down[t % 2].product(64 * u, 64 * Eu)
+            bound = bound + tight.U * (np.abs(want) + bound)
+            err = np.abs(y[t].double().cpu().numpy() - want[0])
+            assert (err <= bound[0]).all(), "token %d: worst err/bound %.3g" % (t, (err / bound[0]).max())
+        layer.free()

@@ -103,6 +103,7 @@ def _bind(lib):
         "wq_moe_create": (ci, [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp), ci, ctypes.POINTER(vp)]),
         "wq_moe_free": (ci, [vp]),
         "wq_moe_ffn_dev": (ci, [vp, vp, ci, ci, cl, vp, vp, ci, vp, cl, vp, cl, vp]),
+        "wq_describe_moe": (ci, [vp, ci, ci, ci, cl, ctypes.c_char_p, ctypes.c_size_t]),
         "wq_rope_create": (ci, [ci, ci, ctypes.c_double, _c_int_p, ci, ctypes.POINTER(vp)]),
         "wq_rope_dev": (ci, [vp, ci, vp, ci, ci, ci, ci, cl, cl, vp, cl, vp, cl, cl, vp]),
         "wq_rope_free": (ci, [vp]),
@@ -767,3 +768,10 @@ def wq_moe_ffn_dev(moe: Moe, x, ids, weights, y, add=None, stream=None) -> None:
                             ys[0], _raw_stream(stream, dev))
     if rc:
         _check(rc, "wq_moe_ffn_dev")
+
+
+def wq_describe_moe(moe: Moe, dtype: int, T: int, k: int, x_stride: int = None) -> str:
+    """The plan of wq_moe_ffn_dev for T tokens with k experts each as text (x_stride None: contiguous rows)."""
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.wq_describe_moe(moe.ptr, dtype, _int(T), _int(k), moe.D if x_stride is None else x_stride, buf, len(buf)), "wq_describe_moe")
+    return buf.value.decode()

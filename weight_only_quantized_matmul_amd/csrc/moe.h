@@ -63,7 +63,7 @@ constexpr int kInlineSlots = 256; // up to as many, the products' blocks find th
 // ---------------------------------------------------------------------------
 struct MoeArgs {
     const MoeExpert *experts;
-    int E, T, k, cus;
+    int E, T, k;
     const int *ids;       // [T, k]
     const float *weights; // [T, k]
     const void *x, *add;
@@ -76,9 +76,8 @@ struct MoeArgs {
     int xe_n, x_size;
     bool x_bf16;
     int ldh;                 // floats a row of h, a multiple of four
-    int active;              // experts that some token chose, on average of an even choice
-    int operands;            // of 16 stacked rows, four activations each, that the products take at a time: 1, 2; 4, 8: prepared parts
-    int tiles_in, tiles_out; // tiles of outputs a block of the products takes
+    int operands;              // 1, 2; 4, 8: activations in prepared parts
+    MoeForm form_in, form_out; // of gate and up, of down
     // workspace
     MoeWork *plan; // min(E, N), those without rows last; null: the products' blocks plan for themselves
     int *order;    // N slots, with a plan

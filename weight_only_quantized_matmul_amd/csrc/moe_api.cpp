@@ -1,5 +1,6 @@
 // C entry points of the mixture-of-experts operators (include/wqmm.h): argument checks and launches.
 #include <cmath>
+#include <cstdio>
 #include <new>
 
 #include "entry.h"
@@ -34,6 +35,60 @@ wq::MoeMatrix matrix_of(const wq_tensor *t) {
     m.w = t->d_w;
     m.scales = t->gs > 0 ? t->d_scales_t : t->d_scales;
     return m;
+}
+
+// Where a call's workspace holds what, in bytes from its start.
+struct Layout {
+    bool parts, apart, planned;
+    size_t order, copy, h, d, xp, hp, xunit, hunit, bytes;
+};
+
+// How a call runs: everything of `a` but its buffers, and their places in the workspace. size: bytes of an element of x; x_vec: x
+// is aligned to four of them.
+int plan_moe(const wq_moe *moe, int size, int T, int k, long x_stride, bool x_vec, int cus, wq::MoeArgs *args, Layout *layout) {
+    wq::MoeArgs &a = *args;
+    Layout &l = *layout;
+    a.experts = moe->d_experts;
+    a.E = moe->E;
+    a.T = T;
+    a.k = k;
+    a.in = moe->in;
+    a.out = moe->out;
+    const long N = (long)T * k;
+    a.x_size = size;
+    a.xe_n = (a.in.I + 3) / 4 * 4;
+    a.ldh = (a.in.O + 3) / 4 * 4;
+    // experts that some token chose, on average of an even choice
+    int active = (int)(a.E * (1.0 - std::pow(1.0 - (k < a.E ? k : a.E) / (double)a.E, T)) + 0.5);
+    if (active < 1) active = 1;
+    // Operands for the rows that an expert has on average, with room for those that have more. 17 tokens on 64 experts of 768 x
+    // 2048 in int4 (2.4 rows) 44.3 us with two, 48.6 with one, 56.3 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
+    // 126 us with eight, 159 with four, 232 with two; one token 34.8 us with one, 36.7 with two.
+    const double rows = (double)N / active;
+    a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
+    // (of the products' blocks, of 256 threads, as many as their smallest tiles of outputs make)
+    const double pairs = N <= wq::kInlineSlots || N < a.E ? N : a.E;
+    if ((double)T * (a.out.O + 255.0) > wq::kMaxThreads || (double)N * a.out.kp / 16 > wq::kMaxThreads ||
+        pairs * (a.in.O + 15.0) * 16 > wq::kMaxThreads || pairs * (a.out.O + 31.0) * 8 > wq::kMaxThreads)
+        return WQ_E_UNSUPPORTED;
+    const int epb = wq::elems_per_byte(moe->fmt);
+    const auto turned = [&](const wq::MoeShape &s) { return s.gs > 0 && s.gs % (64 * epb) != 0; };
+    a.form_in = wq::moe_form(true, a.in.O, a.in.steps, turned(a.in), a.operands, active, cus);
+    a.form_out = wq::moe_form(false, a.out.O, a.out.steps, turned(a.out), a.operands, active, cus);
+    l.parts = a.operands >= 4;
+    l.apart = !l.parts && (a.in.I % 4 != 0 || x_stride % 4 != 0 || !x_vec);
+    l.planned = N > wq::kInlineSlots || l.apart || l.parts;
+    const auto room = [](double bytes) { return (size_t)wq::round_up((long)bytes, 256); };
+    l.order = l.planned ? room((double)(N < a.E ? N : a.E) * sizeof(wq::MoeWork)) : 0;
+    l.copy = l.order + (l.planned ? room(4.0 * N) : 0);
+    l.h = l.copy + (l.apart ? room((double)T * a.xe_n * size) : 0);
+    l.d = l.h + room(4.0 * N * a.ldh);
+    l.xp = l.d + room(4.0 * N * a.out.O);
+    l.hp = l.xp + (l.parts ? (size_t)T * a.in.steps * 512 * epb : 0);
+    l.xunit = l.hp + (l.parts ? (size_t)N * a.out.steps * 512 * epb : 0);
+    l.hunit = l.xunit + (l.parts ? room(4.0 * T * a.in.steps) : 0);
+    l.bytes = l.hunit + (l.parts ? (size_t)4 * N * a.out.steps : 0);
+    return WQ_OK;
 }
 
 } // namespace
@@ -135,11 +190,8 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     if (rc != WQ_OK) return rc;
     DeviceScope scope(moe->device);
     wq::MoeArgs a;
-    a.experts = moe->d_experts;
-    a.E = moe->E;
-    a.cus = wq::device_cus(moe->device);
-    a.T = T;
-    a.k = k;
+    Layout l;
+    if ((rc = plan_moe(moe, size, T, k, x_stride, aligned(x, 4 * size), wq::device_cus(moe->device), &a, &l)) != WQ_OK) return rc;
     a.ids = ids;
     a.weights = weights;
     a.x = x;
@@ -148,51 +200,41 @@ int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_st
     a.xs = x_stride;
     a.as = add_stride;
     a.ys = y_stride;
-    a.in = moe->in;
-    a.out = moe->out;
-    const long N = (long)T * k;
-    a.x_size = size;
     a.x_bf16 = dtype == WQ_DT_BF16;
-    a.xe_n = (a.in.I + 3) / 4 * 4;
-    a.ldh = (a.in.O + 3) / 4 * 4;
-    a.active = (int)(a.E * (1.0 - std::pow(1.0 - (k < a.E ? k : a.E) / (double)a.E, T)) + 0.5);
-    if (a.active < 1) a.active = 1;
-    // Operands for the rows that an expert has on average, with room for those that have more. 17 tokens on 64 experts of 768 x
-    // 2048 in int4 (2.4 rows) 44.3 us with two, 48.6 with one, 56.3 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
-    // 126 us with eight, 159 with four, 232 with two; one token 34.8 us with one, 36.7 with two.
-    const double rows = (double)N / a.active;
-    // (of the products' blocks, of 256 threads, as many as their smallest tiles of outputs make)
-    const double pairs = N <= wq::kInlineSlots || N < a.E ? N : a.E;
-    if ((double)T * (a.out.O + 255.0) > wq::kMaxThreads || (double)N * a.out.kp / 16 > wq::kMaxThreads ||
-        pairs * (a.in.O + 15.0) * 16 > wq::kMaxThreads || pairs * (a.out.O + 31.0) * 8 > wq::kMaxThreads)
-        return WQ_E_UNSUPPORTED;
-    a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
-    const bool parts = a.operands >= 4;
-    const bool apart = !parts && (a.in.I % 4 != 0 || x_stride % 4 != 0 || !aligned(x, 4 * size));
-    const bool planned = N > wq::kInlineSlots || apart || parts;
-    const size_t plan = planned ? (size_t)wq::round_up((N < a.E ? N : a.E) * sizeof(wq::MoeWork), 256) : 0;
-    const size_t order = planned ? (size_t)wq::round_up(4 * N, 256) : 0;
-    const size_t copy = apart ? (size_t)wq::round_up((long)T * a.xe_n * size, 256) : 0;
-    const size_t h = (size_t)wq::round_up(4 * N * a.ldh, 256);
-    const int epb = wq::elems_per_byte(moe->fmt);
-    const size_t d = (size_t)wq::round_up(4 * N * a.out.O, 256);
-    const size_t xp = parts ? (size_t)T * a.in.steps * 512 * epb : 0, hp = parts ? (size_t)N * a.out.steps * 512 * epb : 0;
-    const size_t xu = parts ? (size_t)wq::round_up(4L * T * a.in.steps, 256) : 0, hu = parts ? (size_t)4 * N * a.out.steps : 0;
     void *ws = nullptr;
-    if ((rc = wq::stream_workspace(moe->device, plan + order + copy + h + d + xp + hp + xu + hu, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
+    if ((rc = wq::stream_workspace(moe->device, l.bytes, (hipStream_t)hip_stream, &ws)) != WQ_OK) return rc;
     char *at = (char *)ws;
-    a.plan = planned ? (wq::MoeWork *)at : nullptr;
-    a.order = (int *)(at += plan);
-    a.copy = apart ? at + order : nullptr;
-    a.h = (float *)(at += order + copy);
-    a.d = (float *)(at += h);
-    a.xp = parts ? (uint8_t *)at + d : nullptr;
-    a.hp = a.xp + xp;
-    a.xunit = (float *)(at + d + xp + hp);
-    a.hunit = (float *)(at + d + xp + hp + xu);
-    a.xe = apart ? a.copy : x;
-    a.xes = apart ? a.xe_n : x_stride;
+    a.plan = l.planned ? (wq::MoeWork *)at : nullptr;
+    a.order = (int *)(at + l.order);
+    a.copy = l.apart ? at + l.copy : nullptr;
+    a.h = (float *)(at + l.h);
+    a.d = (float *)(at + l.d);
+    a.xp = l.parts ? (uint8_t *)at + l.xp : nullptr;
+    a.hp = l.parts ? (uint8_t *)at + l.hp : nullptr;
+    a.xunit = (float *)(at + l.xunit);
+    a.hunit = (float *)(at + l.hunit);
+    a.xe = l.apart ? a.copy : x;
+    a.xes = l.apart ? a.xe_n : x_stride;
     return status(wq::launch_moe(a, moe->fmt, dtype, (hipStream_t)hip_stream));
+}
+
+int wq_describe_moe(const wq_moe *moe, int dtype, int T, int k, long x_stride, char *buf, size_t buflen) {
+    if (moe == nullptr || moe->magic != wq::kMoeMagic || !float_type(dtype) || T <= 0 || k <= 0 || x_stride < 0 || buf == nullptr || buflen == 0)
+        return WQ_E_INVAL;
+    if ((long)T * k > WQ_MOE_MAX_ROWS) return WQ_E_UNSUPPORTED;
+    wq::MoeArgs a;
+    Layout l;
+    const int rc = plan_moe(moe, size_of(dtype), T, k, x_stride, true, wq::device_is_open(moe->device) ? wq::device_cus(moe->device) : 256, &a, &l);
+    if (rc != WQ_OK) return rc;
+    char text[2][96];
+    for (int i = 0; i < 2; ++i) {
+        const wq::MoeForm &f = i ? a.form_out : a.form_in;
+        const int pos = 128 * wq::elems_per_byte(moe->fmt), rows = wq::moe_rows(f.m, f.wk, pos), all = wq::moe_steps((i ? a.out : a.in).steps, f.wk);
+        const int one = wq::moe_phase(f.m, f.wk, pos, 1, all), full = wq::moe_phase(f.m, f.wk, pos, rows, all);
+        snprintf(text[i], sizeof text[i], "operands=%d waves=%d tiles=%d rows=%d phases=%d-%d", f.m, f.wk, f.tiles, rows, (all + one - 1) / one, (all + full - 1) / full);
+    }
+    snprintf(buf, buflen, "in %s out %s plan=%d copy=%d workspace=%zu", text[0], text[1], (int)l.planned, (int)l.apart, l.bytes);
+    return WQ_OK;
 }
 
 } // extern "C"

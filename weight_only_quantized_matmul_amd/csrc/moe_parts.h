@@ -23,7 +23,7 @@ constexpr float kBack = 0x1p16f;
 // Bytes of b where sel's are 0..3, of a where 4..7.
 __device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t sel) { return __builtin_amdgcn_perm(a, b, sel); }
 
-constexpr int kPiece = 16; // positions that a thread makes parts of
+constexpr int kPiece = kMoePiece;
 
 // The parts of 16 neighbouring positions' activations x, in the order in which the codes come out of their words, and the unit
 // of the step that they belong to, of all of whose pieces the lanes come here together.

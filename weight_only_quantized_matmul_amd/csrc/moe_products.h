@@ -19,11 +19,10 @@
 namespace wq {
 namespace {
 
-// How a block's four waves share its work: WR groups of output rows, WK waves along the rows' bytes. A wave has NT tiles of
-// 16 rows of weights (gate and up of the same 16 outputs, or 32 outputs of down), so a block makes 16 * WR (32 * WR) outputs
-// at a time, a tile of them; it takes several tiles of one expert one after another.
-constexpr int kWaves = 4;
-constexpr int NT = 2;
+// (How a block's waves share its work: moe_plan.h.) A block makes a tile of outputs at a time; it takes several tiles of one
+// expert one after another.
+constexpr int kWaves = kMoeWaves;
+constexpr int NT = kMoeTiles;
 // Pointers read from the experts' table are of no known address space otherwise, and their loads would count as LDS loads too.
 #define GLOBAL __attribute__((address_space(1)))
 
@@ -34,21 +33,17 @@ template <int FMT, bool GATED, int GS, int M, int WK>
 struct Products {
     using F = Fmt<FMT>;
     static constexpr int WR = kWaves / WK;
-    static constexpr int OUT = (GATED ? 16 : 16 * NT) * WR; // outputs of a block
+    static constexpr int OUT = moe_outputs(GATED, WK);      // outputs of a block
     static constexpr int UNITS = F::EPB;                    // products of 64 positions in 64 bytes
     static constexpr bool TURN = GS == 2 && F::EPB > 1;
     static constexpr int RED = kWaves * NT * 64 * 4;        // bytes of the waves' sums
-    // Many rows: two blocks a CU with more registers, else three; and activations whose parts stand prepared in memory, where
-    // every block would make them again (8 experts of 2048 x 6144 in int8 with 16 rows each: 190 us).
-    static constexpr bool BIG = M >= 3;
-    // Bytes of a phase's parts and units: with the waves' sums and the slots, a third (half) of a CU's 160 KB. (Three blocks
-    // with 44 KB: 5 tokens on 8 experts of 2048 x 6144 in int2 33.7 us instead of 32.9.)
-    static constexpr int LDS = BIG ? 74 * 1024 : 99 * 512;
-    static constexpr int UNIT = 4 * (2 * WK * F::POS + 16) + 4 * 2 * WK; // bytes of an activation row with two steps of every wave
-    static constexpr int ROWS = LDS / UNIT < 4 * M ? LDS / UNIT : 4 * M; // rows at a time
+    // Many rows: activations whose parts stand prepared in memory, where every block would make them again (8 experts of
+    // 2048 x 6144 in int8 with 16 rows each: 190 us).
+    static constexpr bool BIG = moe_big(M);
+    static constexpr int LDS = moe_lds(M), ROWS = moe_rows(M, WK, F::POS);
     static_assert(ROWS >= 1, "a phase holds two steps of every wave");
     static constexpr int PIECE = kPiece;                    // positions that a thread stages at a time
-    static constexpr int PRE = M == 8 ? 0 : 2;                     // pieces of a thread that are loaded ahead of the weights
+    static constexpr int PRE = moe_ahead(M);
 
     const MoeArgs &a;
     const MoeShape &sh;
@@ -119,13 +114,7 @@ struct Products {
 
     // Output tiles [t0, t1) of n rows, the expert's slots; n <= ROWS.
     __device__ __forceinline__ void rows(const int *slots, int n, int t0, int t1) {
-        // a wave's steps of a tile are wk, wk + WK, ...; all waves take an even number of them, past the row on activations of 0
-        const int all = ((sh.steps + WK - 1) / WK + 1) & ~1;
-        // a phase: as many steps of all waves as the buffer holds activations of
-        const int fit = (LDS / n - 64) / (WK * (4 * F::POS + 4)) & ~1;
-        // (BIG: no more than what the threads hold ahead)
-        const int held = BIG && PRE > 0 ? max(PRE * 64 * kWaves * PIECE / (n * WK * F::POS) & ~1, 2) : fit;
-        const int per = min(all, min(fit, held)), phases = (all + per - 1) / per; // per is even
+        const int all = moe_steps(sh.steps, WK), per = moe_phase(M, WK, F::POS, n, all), phases = (all + per - 1) / per;
         const int span = per * WK * F::POS, pitch = span + 16;         // positions; bytes of a part's row, 16 apart in the banks
         float *units = reinterpret_cast<float *>(lds + n * 4 * pitch); // [n][per * WK]
         // pieces of a phase: `row` of each slot (the last phase: `rest`); i / row for i, row < 2^16 by its reciprocal
@@ -383,7 +372,7 @@ __global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kern
     __shared__ int here[INLINE ? kInlineSlots : 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const MoeShape &sh = GATED ? a.in : a.out;
-    const int tiles = (sh.O + P::OUT - 1) / P::OUT, per = GATED ? a.tiles_in : a.tiles_out;
+    const int tiles = (sh.O + P::OUT - 1) / P::OUT, per = GATED ? a.form_in.tiles : a.form_out.tiles;
     const int t0 = blockIdx.x * per, t1 = min(t0 + per, tiles);
     auto work = [&](const MoeMatrix &m0, const MoeMatrix &m1) {
         return P{a, sh, m0, m1, wave / WK, wave % WK, lane, lane & 15, lane >> 4, lds, red};
@@ -441,15 +430,11 @@ __global__ __launch_bounds__(64 * kWaves, M >= 3 ? 2 : 3) void moe_products_kern
 }
 
 template <int FMT, bool GATED, int GS, int M, int WK>
-hipError_t launch_products(MoeArgs &a, int active, hipStream_t st) {
+hipError_t launch_products(MoeArgs &a, hipStream_t st) {
     const MoeShape &sh = GATED ? a.in : a.out;
     const long N = (long)a.T * a.k;
     using P = Products<FMT, GATED, GS, M, WK>;
-    const int tiles = (sh.O + P::OUT - 1) / P::OUT;
-    // as many tiles a block as leave three blocks a CU; of the large form, which would stage its activations anew, one
-    int per = P::BIG ? 1 : (int)((long)tiles * active / (3 * a.cus));
-    per = per < 1 ? 1 : per > tiles ? tiles : per;
-    (GATED ? a.tiles_in : a.tiles_out) = per;
+    const int tiles = (sh.O + P::OUT - 1) / P::OUT, per = GATED ? a.form_in.tiles : a.form_out.tiles;
     const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)(a.plan == nullptr ? N : N < a.E ? N : a.E));
     if constexpr (!P::BIG) {
         if (a.plan == nullptr) {
@@ -463,26 +448,28 @@ hipError_t launch_products(MoeArgs &a, int active, hipStream_t st) {
 }
 
 template <int FMT, bool GATED, int GS, int M>
-hipError_t launch_wk(MoeArgs &a, int active, hipStream_t st) {
-    const MoeShape &sh = GATED ? a.in : a.out;
-    // Waves along the rows' bytes only as far as the outputs alone leave CUs with less than two blocks, and rows of some length:
-    // one token, 8 experts of 2048 x 6144 in int4 34.4 us with two for both products, 36.9 with one, 38.7 with four; 17 tokens on
-    // 64 experts of 768 x 2048 46.6 us with one, 50.3 with two; 5 tokens on 8 experts in int2 33.3 with two, 42.9 with four.
-    const int out = (GATED ? 16 : 16 * NT) * kWaves;
-    const long most = (long)active * ((sh.O + out - 1) / out); // blocks with none of them
-    if (most >= 2 * a.cus || sh.steps < 4) return launch_products<FMT, GATED, GS, M, 1>(a, active, st);
-    if (most >= a.cus || sh.steps < 16) return launch_products<FMT, GATED, GS, M, 2>(a, active, st);
-    return launch_products<FMT, GATED, GS, M, 4>(a, active, st);
+hipError_t launch_wk(MoeArgs &a, hipStream_t st) {
+    switch (GATED ? a.form_in.wk : a.form_out.wk) {
+    case 1: return launch_products<FMT, GATED, GS, M, 1>(a, st);
+    case 2: return launch_products<FMT, GATED, GS, M, 2>(a, st);
+    default: return launch_products<FMT, GATED, GS, M, 4>(a, st);
+    }
 }
 
 template <int FMT, bool GATED, int GS>
 hipError_t launch_m(MoeArgs &a, hipStream_t st) {
-    switch (a.operands) {
-    case 1: return launch_wk<FMT, GATED, GS, 1>(a, a.active, st);
-    case 2: return launch_wk<FMT, GATED, GS, 2>(a, a.active, st);
-    case 4: return launch_wk<FMT, GATED, GS, GS == 2 ? 3 : 4>(a, a.active, st);
-    default: // (of turned operands, more than three would spill)
-        return launch_wk<FMT, GATED, GS, GS == 2 ? 3 : 8>(a, a.active, st);
+    switch (GATED ? a.form_in.m : a.form_out.m) {
+    case 1: return launch_wk<FMT, GATED, GS, 1>(a, st);
+    case 2: return launch_wk<FMT, GATED, GS, 2>(a, st);
+    case 3:
+        if constexpr (GS == 2) return launch_wk<FMT, GATED, GS, 3>(a, st);
+        return hipErrorInvalidValue;
+    case 4:
+        if constexpr (GS != 2) return launch_wk<FMT, GATED, GS, 4>(a, st);
+        return hipErrorInvalidValue;
+    default:
+        if constexpr (GS != 2) return launch_wk<FMT, GATED, GS, 8>(a, st);
+        return hipErrorInvalidValue;
     }
 }
 
