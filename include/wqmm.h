@@ -567,7 +567,8 @@ enum wq_gating { WQ_GATE_SOFTMAX = 0, WQ_GATE_SIGMOID = 1 };
  * divided by the sum of the k if `normalise`, times scale. Of equal values the
  * lower index goes first. p, c and sums are fp64. A NaN score counts as -inf,
  * +inf as the largest fp32; where softmax sees -inf only, every p is 0; a sum of
- * 0 leaves weights of 0. A NaN c counts as -inf.
+ * 0 leaves weights of 0. A NaN c counts as -inf, and so does a group's value
+ * that is none (its two largest c are +inf and -inf).
  * 1 <= k <= E / groups * top_groups. WQ_E_UNSUPPORTED: E > WQ_MOE_MAX_EXPERTS,
  * groups > WQ_MOE_MAX_GROUPS, k > WQ_MOE_MAX_K. T == 0 is a no-op.
  */
@@ -597,20 +598,23 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * of a batch without a token, an expert that lives elsewhere); an expert that
  * stands twice counts twice. y may be x or add (same stride).
  * The products take codes as they are, and activations (x, and h in fp32) as
- * integers of up to 31 bits: whole multiples of a power of two that the 128
- * (int8 weights), 256 (int4) or 512 (int2) neighbours which meet the same 128
- * bytes of a row share, each within 2^-30 of the largest magnitude among them
- * (magnitudes below 2^-96: within 2^-126). Sums over those are exact, sums over
- * the row fp32 (with group scales within 2^-126 besides), the sum over j
- * fp32 in the order of j, y rounded once. An
- * infinity or NaN in x, or an h that overflows, makes that expert's row for the
+ * integers of up to 31 bits: whole multiples of a power of two that those share
+ * which meet the same 128 bytes of a resident row (128 elements with int8
+ * weights, 256 with int4, 512 with int2, not all side by side), each within
+ * 2^-30 of the largest magnitude among them (magnitudes below 2^-96: within
+ * 2^-126). Sums over those are exact (with group scales over parts of them),
+ * sums over the row fp32 and, with group scales, within 2^-126; the sum over j
+ * is fp32 in the order of j, y rounded once. An infinity or NaN in x, or an h
+ * that overflows, makes that expert's row for the
  * token NaN. What a token gets does not depend on what the other tokens hold
  * or chose; their number chooses among forms that split the sums differently.
  * It uses the stream's workspace as wq_matmul_dev's tiled path does (it may
  * grow, but not while the stream is being captured).
- * For many tokens an expert the grouped calls are faster; T * k above
- * WQ_MOE_MAX_ROWS, or shapes whose launches could have 2^32 threads (16 * F, 8 *
- * D_out times min(E, T * k)), give WQ_E_UNSUPPORTED. T == 0 is a no-op.
+ * T * k above WQ_MOE_MAX_ROWS, or shapes whose launches could have 2^32 threads
+ * (16 * F, 8 * D_out times min(E, T * k)), give WQ_E_UNSUPPORTED. Up to there it
+ * takes less time than wq_swiglu_ffn_dev on rows gathered by expert (which takes
+ * activations in 24 bits whatever their neighbours are), but for about 1024 rows
+ * an expert and more. T == 0 is a no-op.
  */
 int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
                    int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream);
