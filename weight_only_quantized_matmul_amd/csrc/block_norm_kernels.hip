@@ -7,8 +7,8 @@
 // One block takes one row and holds it in registers as fp32 from the only read
 // of x, gate and residual to the only write of r and y; two block-wide sums.
 // Memory bounds it: 8191 rows of 6144 in bf16, 503 MB, 93.6 us, 5.4 TB/s (a
-// large copy: 4.8; part of 503 MB stays in the 256 MB cache behind the L2 from
-// pass to pass); one row is latency, 3.9 us with two barriers in a row.
+// large copy: 4.8, an elementwise sum 6.2; part of 503 MB stays in the 256 MB
+// cache behind the L2 from pass to pass); one row is latency, 3.9 us with two barriers in a row.
 #include "rows.h"
 
 namespace wq {

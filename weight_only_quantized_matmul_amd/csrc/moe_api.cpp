@@ -62,8 +62,8 @@ int plan_moe(const wq_moe *moe, int size, int T, int k, long x_stride, bool x_ve
     int active = (int)(a.E * (1.0 - std::pow(1.0 - (k < a.E ? k : a.E) / (double)a.E, T)) + 0.5);
     if (active < 1) active = 1;
     // Operands for the rows that an expert has on average, with room for those that have more. 17 tokens on 64 experts of 768 x
-    // 2048 in int4 (2.4 rows) 44.3 us with two, 48.6 with one, 56.3 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
-    // 126 us with eight, 159 with four, 232 with two; one token 34.8 us with one, 36.7 with two.
+    // 2048 in int4 (2.4 rows) 42.1 us with two, 45.3 with one, 55.2 with four; 64 tokens on 8 of 2048 x 6144 in int8 (16 rows)
+    // 115 us with eight, 154 with four, 213 with two; one token 34.4 us with one, 36.2 with two.
     const double rows = (double)N / active;
     a.operands = T <= 4 || rows <= 1.6 ? 1 : T <= 8 || rows <= 4 ? 2 : T <= 16 || rows <= 10 ? 4 : 8;
     // (of the products' blocks, of 256 threads, as many as their smallest tiles of outputs make)

@@ -84,10 +84,11 @@ struct MoeForm {
 // do not cover whole halves of a step; active: experts that some token chose.
 constexpr MoeForm moe_form(bool gated, int O, int steps, bool turned, int operands, int active, int cus) {
     MoeForm f{0, 0, 0};
-    f.m = operands >= 4 && turned ? 3 : operands; // (of turned operands, more than three would spill)
+    f.m = operands >= 4 && turned ? 3 : operands; // (of turned operands, more than three would spill; in int2 three do)
     // Waves along the rows' bytes only as far as the outputs alone leave CUs with less than two blocks, and rows of some length:
-    // one token, 8 experts of 2048 x 6144 in int4 34.4 us with two for both products, 36.9 with one, 38.7 with four; 17 tokens on
-    // 64 experts of 768 x 2048 46.6 us with one, 50.3 with two; 5 tokens on 8 experts in int2 33.3 with two, 42.9 with four.
+    // one token, 8 experts of 2048 x 6144 in int4 34.4 us with two for both products, 36.7 with one, 38.9 with four; 17 tokens on
+    // 64 experts of 768 x 2048 42.2 us with one, 49.0 with two; 5 tokens on 8 experts in int2 34.8 with two, 40.2 with one, 42.9
+    // with four.
     const int out = moe_outputs(gated, 1);
     const long most = (long)active * ((O + out - 1) / out); // blocks with none of them
     f.wk = most >= 2 * cus || steps < 4 ? 1 : most >= cus || steps < 16 ? 2 : 4;

@@ -6,10 +6,11 @@
 // meet: 128, 256 or 512 of them) share, and that as four signed base-256 digits, its parts: x = unit * sum_p d_p 256^p within
 // 2^-30 of the step's largest magnitude. The integer sums are exact; each step's goes to the fp32 sum with its unit.
 //
-// With a few rows an expert the weights' stream bounds them, read once at up to 4.8 TB/s (a large copy's rate): one token on 8
-// experts of 2048 x 6144 in int4, 151 MB, 20.2 us (gate and up: 4.9 TB/s) and 12.8 us (down: 3.9 TB/s). Loads of the next two
-// steps are always in flight, across tiles too. With more rows reading the operands from LDS bounds them, 16 stacked rows a
-// KiB: 64 tokens on 8 experts of the same shape in int8, 302 MB, 66.8 and 42.6 us (2.8 TB/s), 126 us with all launches.
+// With a few rows an expert the weights' stream bounds them, read once: one token on 8 experts of 2048 x 6144 in int4, 151 MB,
+// 20.4 us (gate and up: 4.9 TB/s) and 11.2 us (down: 4.5 TB/s; a large copy 4.8), 34.5 us with all launches; in int8 57 us, in
+// int2 26 us. Loads of the next two steps are always in flight, across tiles too. With more rows reading the operands from LDS
+// bounds them, 16 stacked rows a KiB: 64 tokens on 8 experts of the same shape in int8, 302 MB, 62.4 and 40.3 us (3.2 and 2.5
+// TB/s), 119 us with all launches.
 #pragma once
 
 #include <type_traits>
@@ -38,7 +39,7 @@ struct Products {
     static constexpr bool TURN = GS == 2 && F::EPB > 1;
     static constexpr int RED = kWaves * NT * 64 * 4;        // bytes of the waves' sums
     // Many rows: activations whose parts stand prepared in memory, where every block would make them again (8 experts of
-    // 2048 x 6144 in int8 with 16 rows each: 190 us).
+    // 2048 x 6144 in int8 with 16 rows each: 190 us instead of 126).
     static constexpr bool BIG = moe_big(M);
     static constexpr int LDS = moe_lds(M), ROWS = moe_rows(M, WK, F::POS);
     static_assert(ROWS >= 1, "a phase holds two steps of every wave");

@@ -11,7 +11,7 @@
 // One token (256 experts in 8 groups, 8 chosen) is latency: 6.6 us, a chain
 // of fp64 exponentials and k maxima, each of which waits for the last. A prompt
 // of 8191 tokens over 128 experts is bound by the fp64 and integer work of the
-// vector units: 13.7 us, 2.6 MB at 0.2 TB/s.
+// vector units: 12.7 us, 2.6 MB at 0.2 TB/s.
 #include "moe.h"
 
 namespace wq {
