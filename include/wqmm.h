@@ -612,8 +612,9 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * grow, but not while the stream is being captured).
  * T * k above WQ_MOE_MAX_ROWS, or shapes whose launches could have 2^32 threads
  * (16 * F, 8 * D_out times min(E, T * k)), give WQ_E_UNSUPPORTED. Up to there it
- * takes less time than wq_swiglu_ffn_dev on rows gathered by expert (which takes
- * activations in 24 bits whatever their neighbours are), but for about 1024 rows
+ * takes less time than wq_swiglu_ffn_dev on a group of all experts with rows
+ * gathered by expert (which keeps 24 bits of each activation, whatever is
+ * multiplied beside it), but for about 1024 rows
  * an expert and more. T == 0 is a no-op.
  */
 int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,

@@ -16,3 +16,12 @@ def test_bounds(tmp_path):
     assert b.returncode == 0, b.stderr[-3000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout[-2000:]
+
+
+def test_description_is_refused_without_a_layer():
+    import ctypes
+
+    import weight_only_quantized_matmul_amd as wq
+
+    buf = ctypes.create_string_buffer(64)
+    assert wq.lib.wq_describe_moe(None, wq.WQ_DT_F32, 1, 1, 64, buf, len(buf)) == wq.WQ_E_INVAL
