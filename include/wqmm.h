@@ -605,17 +605,17 @@ int wq_moe_free(wq_moe *moe); /* NULL is a no-op */
  * 2^-126). Sums over those are exact (with group scales over parts of them),
  * sums over the row fp32 and, with group scales, within 2^-126; the sum over j
  * is fp32 in the order of j, y rounded once. An infinity or NaN in x, or an h
- * that overflows, makes that expert's row for the
- * token NaN. What a token gets does not depend on what the other tokens hold
- * or chose; their number chooses among forms that split the sums differently.
+ * that overflows, makes that expert's row for the token NaN. What a token gets
+ * does not depend on what the other tokens hold or chose; their number chooses
+ * among forms that split the sums differently.
  * It uses the stream's workspace as wq_matmul_dev's tiled path does (it may
  * grow, but not while the stream is being captured).
  * T * k above WQ_MOE_MAX_ROWS, or shapes whose launches could have 2^32 threads
  * (16 * F, 8 * D_out times min(E, T * k)), give WQ_E_UNSUPPORTED. Up to there it
  * takes less time than wq_swiglu_ffn_dev on a group of all experts with rows
  * gathered by expert (which keeps 24 bits of each activation, whatever is
- * multiplied beside it), but for about 1024 rows
- * an expert and more. T == 0 is a no-op.
+ * multiplied beside it), but for about 1024 rows an expert and more. T == 0 is
+ * a no-op.
  */
 int wq_moe_ffn_dev(const wq_moe *moe, const void *x, int dtype, int T, long x_stride, const int *ids, const float *weights,
                    int k, const void *add, long add_stride, void *y, long y_stride, void *hip_stream);
